@@ -79,6 +79,13 @@ __host__ __device__ __forceinline__ bool sees(int i, int j, int window, int n_si
   return j <= i && (i - j < window || j < n_sink);
 }
 
+// Whether token i sees itself and no other key.  Its probability is then 1 whatever the score, and the score's gradient
+// P (dP - delta) exactly zero; computed, dP and delta are two sums of the same numbers in different orders, and their
+// difference is noise that would be all there is of dQ, and of dK where a key is seen by such rows alone.
+__host__ __device__ __forceinline__ bool sees_one(int i, int window, int n_sink) {
+  return i == 0 || (window == 1 && n_sink == 0);
+}
+
 template <typename T>
 __device__ __forceinline__ T* head_row(const mlora_heads& t, long long row, int h) {
   return static_cast<T*>(t.data) + row * t.row_stride + h * t.head_stride;

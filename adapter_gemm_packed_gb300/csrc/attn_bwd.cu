@@ -302,6 +302,8 @@ __global__ void __launch_bounds__(THREADS<KEYS>, 1) k_attn_bwd(const __grid_cons
 #pragma unroll
             for (int q = 0; q < 2; ++q)
               seen[q] = bits_below(i - row + 1, 32 * q) & (~bits_below(i - A.window + 1 - row, 32 * q) | bits_below(A.n_sink - row, 32 * q));
+            // (a tile that such a row takes part in is never one that all rows see all of)
+            if (sees_one(i, A.window, A.n_sink)) seen[0] = seen[1] = 0;
           }
         }
         const bool all = __all_sync(0xffffffffu, (seen[0] & seen[1]) == 0xffffffffu);
@@ -339,6 +341,7 @@ __global__ void __launch_bounds__(THREADS<KEYS>, 1) k_attn_bwd(const __grid_cons
               if (!all) {
                 if (!(seen[q] >> e & 1)) x0 = y0 = 0.f;
                 if (!(seen[q] >> (e + 1) & 1)) x1 = y1 = 0.f;
+                if (KEYS && q == 0 && e == 0 && row == 0) y0 = 0.f;      // a sequence's first token sees one key
               }
               p[e / 2] = pack_bf16x2(x0, x1);
               ds[e / 2] = pack_bf16x2(y0, y1);
@@ -379,8 +382,10 @@ __global__ void __launch_bounds__(THREADS<KEYS>, 1) k_attn_bwd(const __grid_cons
       OutWarp out{KEYS && b ? &F.g1 : &F.g0, KEYS ? (b ? &A.dk : &A.dv) : &A.dq, sOut + warp * OUT_WARP,
                   it.seq0 + first, w.h, max(0, min(32, it.len - first)), A.D, lane};
       if (!KEYS || b == 1) {
+        // (zero where no token sees more than one key)
+        const float f = KEYS && sees_one(1, A.window, A.n_sink) ? 0.f : A.scale;
 #pragma unroll
-        for (int q = 0; q < NQ; ++q) scale32(o[q], A.scale);
+        for (int q = 0; q < NQ; ++q) scale32(o[q], f);
       }
       if constexpr (NQ == 1) {
         if (32 * q0 < A.D) out.put<1>(32 * q0, &o[0]);

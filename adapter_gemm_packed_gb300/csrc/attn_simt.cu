@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(THREADS<DP>, DP > 64 ? 1 : 3) k_attn_simt_fwd(
 __device__ __forceinline__ void grad_one(const AttnArgs& A, int len, int i, int j, float l2, float delta, float& p, float& ds) {
   const bool ok = i < len && sees(i, j, A.window, A.n_sink);
   p = ok ? exp2f(fmaf(p, A.scale_log2, -l2)) : 0.f;
-  ds = ok ? p * (ds - delta) : 0.f;
+  ds = ok && !sees_one(i, A.window, A.n_sink) ? p * (ds - delta) : 0.f;
 }
 
 // dQ; and delta_i = sum_d dO_id O_id on the way, which the kernel for dK and dV reads after it
