@@ -232,12 +232,10 @@ __device__ __forceinline__ void scale32(uint32_t (&v)[32], float f) {
     v[u] = __float_as_uint(a), v[u + 1] = __float_as_uint(b);
   }
 }
-// columns [u, u + 8) of 32 as bf16
-__device__ __forceinline__ uint4 pack8(const uint32_t (&v)[32], int u) {
-  return make_uint4(pack_bf16x2(__uint_as_float(v[u]), __uint_as_float(v[u + 1])),
-                    pack_bf16x2(__uint_as_float(v[u + 2]), __uint_as_float(v[u + 3])),
-                    pack_bf16x2(__uint_as_float(v[u + 4]), __uint_as_float(v[u + 5])),
-                    pack_bf16x2(__uint_as_float(v[u + 6]), __uint_as_float(v[u + 7])));
+// 32 values as bf16
+__device__ __forceinline__ void pack32(const uint32_t (&v)[32], uint32_t (&p)[16]) {
+#pragma unroll
+  for (int u = 0; u < 16; ++u) p[u] = pack_bf16x2(__uint_as_float(v[2 * u]), __uint_as_float(v[2 * u + 1]));
 }
 
 // A warp's 32 rows of an output tile (a row per lane), 32 columns at a time: through two buffers of 2 KB in shared
@@ -257,13 +255,14 @@ struct OutWarp {
   int row0, h, rows, D, lane;      // the warp's first token, its head, rows that exist (32 or fewer)
   // N (one or two) runs of 32 columns from c0 on
   template <int N>
-  __device__ __forceinline__ void put(int c0, const uint32_t (*v)[32]) {
+  __device__ __forceinline__ void put(int c0, const uint32_t (*p)[16]) {
     if (rows < 32) {
       if (lane < rows) {
         __nv_bfloat16* y = head_row<__nv_bfloat16>(*t, row0 + lane, h) + c0;
 #pragma unroll
         for (int u = 0; u < 32 * N; u += 8)
-          if (c0 + u < D) *reinterpret_cast<uint4*>(y + u) = pack8(v[u / 32], u % 32);      // D is a multiple of 8
+          if (c0 + u < D)      // D is a multiple of 8
+            *reinterpret_cast<uint4*>(y + u) = *reinterpret_cast<const uint4*>(&p[u / 32][u % 32 / 2]);
       }
       return;
     }
@@ -273,7 +272,8 @@ struct OutWarp {
     for (int k = 0; k < N; ++k)
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        *reinterpret_cast<uint4*>(buf + k * OUT_BUF + lane * 64 + ((c ^ (lane >> 1 & 3)) << 4)) = pack8(v[k], 8 * c);
+        *reinterpret_cast<uint4*>(buf + k * OUT_BUF + lane * 64 + ((c ^ (lane >> 1 & 3)) << 4)) =
+            *reinterpret_cast<const uint4*>(&p[k][4 * c]);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if (elect_lane()) {
@@ -291,12 +291,11 @@ struct OutWarp {
 };
 
 // The outputs' low bits.  delta = rowsum(dO O) wants O as the fp32 sums gave it: the error of a rounded O is the
-// same for all of a row's score gradients and does not average out.  Beside each bf16 output the forward keeps the
-// next byte of its fp32 pattern.  Rounding went to the nearest, so that byte, read as signed, is the difference to
-// the rounded pattern in units of 2^8 of the last place.  (What lies below is cut off, at most 2^-15 of the output, and
-// an output that bf16 holds comes back as it is: a row that sees only itself has dP = delta but for fp32 rounding.  An
-// exact tie that went down to even comes back one bf16 step low, no worse than the rounded output itself.)  Rows as in
-// the statistics, 32 rows x 16 columns (bytes) a run, so that a warp's rows are read and written in whole lines.
+// same for all of a row's score gradients and does not average out.  Beside each bf16 output the forward keeps a byte:
+// the difference of its fp32 pattern to the rounded one's in units of 2^8 of the last place, to the nearest, 127 at most.
+// That leaves an error of either sign, at most 2^-16 of the output (2^-15 just below a tie), and an output that lies
+// within half a unit of a bf16 number comes back as that number.  Rows as in the statistics, 32 rows x 16 columns (bytes)
+// a run, so that a warp's rows are read and written in whole lines.
 __device__ __forceinline__ uint8_t* out_low_at(const AttnArgs& A, int chunks, int h, long long s) {
   const long long r = h * A.n_stat + s;
   return A.out_low + (r / 32) * chunks * 512 + (r % 32) * 16;      // + 512 per 16 columns
@@ -308,16 +307,30 @@ __device__ __forceinline__ float out_whole(uint32_t hi, uint32_t l, int k) {
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(l), "r"(0u), "r"((8 + k) * 0x1100 + k * 0x10 + 4));
   return __uint_as_float(hi + d);
 }
-// 32 columns (two runs, from run c on) of this lane's row, into the warp's buffer in shared memory
+// 32 outputs as bf16, to the nearest, ties away from zero: then the lower half of an output's pattern, read as signed, is the
+// difference to the rounded one, ties included.  (Rounding by adding given bits below the last place and cutting off;
+// with half a place for those bits it is rounding to the nearest.)
+__device__ __forceinline__ void pack32_away(const uint32_t (&v)[32], uint32_t (&p)[16]) {
+#pragma unroll
+  for (int u = 0; u < 16; ++u)
+    asm("cvt.rs.bf16x2.f32 %0, %1, %2, %3;"
+        : "=r"(p[u])
+        : "f"(__uint_as_float(v[2 * u + 1])), "f"(__uint_as_float(v[2 * u])), "r"(0x80008000u));
+}
+// The bytes of 32 outputs, two runs from run c on, of this lane's row, into the warp's buffer in shared memory: the
+// differences of two outputs (l), half a unit added, the upper byte kept; differences that this would carry past 127 units
+// stop there (0x7f7e: the lower one's sum may carry into the upper one).  16 sequences of 1024: bytes cut off 137.2
+// microseconds, this 139.4.
 __device__ __forceinline__ void stage_out_low(uint8_t* buf, int c, const uint32_t (&v)[32], int lane) {
+  const auto bytes = [&](int e) {
+    const uint32_t l = __byte_perm(v[e], v[e + 1], 0x5410);
+    return __vmins2(l, 0x7f7e7f7fu) + 0x00800080u;
+  };
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     uint32_t w[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int e = 16 * k + 4 * u;
-      w[u] = __byte_perm(__byte_perm(v[e], v[e + 1], 0x0051), __byte_perm(v[e + 2], v[e + 3], 0x0051), 0x5410);
-    }
+    for (int u = 0; u < 4; ++u) w[u] = __byte_perm(bytes(16 * k + 4 * u), bytes(16 * k + 4 * u + 2), 0x7531);
     *reinterpret_cast<uint4*>(buf + (c + k) * 512 + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }

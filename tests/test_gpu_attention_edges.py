@@ -52,3 +52,54 @@ def test_gradients_of_rows_that_see_one_key_are_zero(lens, window, sinks, hq, hk
     assert all((dq[r] != 0).any() for r in others)
     assert attn.sync_status() == M.MLORA_OK
     attn.close()
+
+
+# ------------------------------------------------------------------ delta
+
+def _delta(attn, lens, h):
+    """delta of head h as the backward left it in `saved`: blocks of 64 rows, 64 logarithms of sums, then 64 delta; each
+    sequence's rows from a multiple of 128 on."""
+    pads = [-(-n // 128) * 128 for n in lens]
+    rows = attn.saved[:2 * sum(pads) * attn.hq].view(attn.hq, -1, 2, 64)[h, :, 1].reshape(-1)
+    return torch.cat([rows[sum(pads[:i]):sum(pads[:i]) + n] for i, n in enumerate(lens)]).double().cpu()
+
+
+@pytest.mark.parametrize("hq,hk,d", [(4, 2, 64), (3, 3, 72), (2, 1, 128), (2, 2, 40)])
+@pytest.mark.parametrize("lens", [[2] * 40, [1, 3, 4, 5, 8, 130, 257], [500, 31]])
+def test_delta_is_made_of_outputs_to_16_bits(lens, hq, hk, d):
+    """delta = rowsum(dO O) from bf16 outputs and the bytes kept beside them.  Queries of zero weigh all visible values
+    the same, which bf16 holds, so that the outputs are known: the values' mean, with many ties between two bf16 numbers
+    where a row sees two or four.  A byte is the difference to the rounded output in units of 2^-8 of its last place, to
+    the nearest (a unit off where 128 of them would be needed): 2^-15 of the output, and fp32 sums."""
+    from adapter_gemm_packed_gb300.attention import WindowAttention
+    attn = WindowAttention(lens, hq, hk, d, 10**6)
+    q, k, v, do = (_draw((attn.n, h, d), i, torch.bfloat16) for i, h in enumerate((hq, hk, hk, hq)))
+    q.zero_()
+    v += 1      # (outputs away from zero)
+    o = attn.forward(q, k, v)
+    attn.backward(q, k, v, o, do)
+    mean = torch.cat([x.cumsum(0) / torch.arange(1, len(x) + 1)[:, None, None]
+                      for x in v.double().cpu().split(lens)]).repeat_interleave(hq // hk, 1)
+    for h in range(hq):
+        terms = do.double().cpu()[:, h] * mean[:, h]
+        err = (_delta(attn, lens, h) - terms.sum(1)).abs()
+        lim = (2.0 ** -15 + 2.0 ** -19) * terms.abs().sum(1)
+        assert (err <= lim).all(), float((err / lim).max())
+    attn.close()
+
+
+def test_delta_is_not_biased():
+    """Gradients of the outputs' signs add up every output's magnitude.  Errors of either sign, half a unit of 2^-15 at
+    most, average out over 128 columns x 900 rows (to 2^-8 of a unit); cut off instead, they would all point one way (a third
+    of a unit and more)."""
+    from adapter_gemm_packed_gb300.attention import WindowAttention
+    attn = WindowAttention([900], 2, 1, 128, 10**6)
+    q, k, v = (_draw((900, h, 128), i, torch.bfloat16) for i, h in enumerate((2, 1, 1)))
+    q.zero_()
+    o = attn.forward(q, k, v)
+    attn.backward(q, k, v, o, torch.sign(o))
+    mean = v.double().cpu().cumsum(0) / torch.arange(1, 901)[:, None, None]
+    for h in range(2):
+        want = (mean[:, 0] * torch.sign(o[:, h].double().cpu())).sum()
+        assert abs(float(_delta(attn, [900], h).sum() - want)) <= 2.0 ** -19 * float(want)
+    attn.close()
