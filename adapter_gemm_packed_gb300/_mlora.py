@@ -86,7 +86,8 @@ class mlora_attention_problem(C.Structure):
 
 class mlora_distill_problem(C.Structure):
     _fields_ = [("n_tokens", C.c_int64), ("vocab", C.c_int32), ("top", C.c_int32), ("dtype", C.c_int32),
-                ("temperature", C.c_float), ("logits_stride", C.c_int64), ("dlogits_stride", C.c_int64)]
+                ("temperature", C.c_float), ("logits_stride", C.c_int64), ("dlogits_stride", C.c_int64),
+                ("flags", C.c_uint32)]
 
 
 class MloraError(RuntimeError):

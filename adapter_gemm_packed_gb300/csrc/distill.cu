@@ -25,7 +25,8 @@
 // another there; which thread adds what goes by an element's place in its row; in rows
 // off a 16-byte boundary, a thread's 16 bytes are put together from two.)
 //
-// Waits have a limit; should one give up, the rows that it concerns get a loss of NaN.
+// Waits have a limit.  Whether one has given up is settled by the computing threads together at the start of every row, so
+// that they never part ways; a block's rows from there on, and the one before, get a loss and a gradient of NaN.
 #include "entry.cuh"
 
 namespace mlora {
@@ -34,8 +35,8 @@ namespace {
 constexpr int THREADS = 384;       // and a warp that fills the ring and one for the teacher's entries
 constexpr int UNROLL = 3;          // 16-byte pieces of a slot per thread
 constexpr int SLOT_VECS = THREADS * UNROLL, SLOT = SLOT_VECS * 16, SLOTS = 6;
-constexpr unsigned long long TIMEOUT_NS = 4000000000ull;
 constexpr int MAX_TOP = 256;
+constexpr int NONE = 0x7fffffff;
 constexpr int AHEAD = 4;           // rows whose teacher's softmax is known ahead of time
 
 struct DistillArgs {
@@ -49,6 +50,8 @@ struct DistillArgs {
   int V, K;
   float T, k2;              // temperature, log2(e) / T
   int same_align;           // rows of z and dz lie the same way to 16-byte boundaries
+  int drop;                 // test hook: the place of a copy that every block leaves out, or -1
+  unsigned long long timeout_ns;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -120,6 +123,17 @@ __device__ __forceinline__ Run warp_sum(Run v) {
 
 // A barrier of the threads that compute.
 __device__ __forceinline__ void sync_threads() { asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory"); }
+
+// A barrier of theirs that tells each whether any of them says so.
+__device__ __forceinline__ bool any_thread(bool v) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(v ? 1u : 0u), "n"(THREADS)
+      : "memory");
+  return any != 0;
+}
 
 // All computing threads get the block's sum.
 __device__ __forceinline__ Run join(Run v, Run* sh) {
@@ -219,6 +233,12 @@ struct Entry {
   float u;       // t, then t / T in base 2
 };
 
+// The block's n-th row.  Each round starts 37 blocks further on: rows of weight zero at a regular distance do not all
+// fall to the same blocks (2048 x 50,001, every fourth row: 100 microseconds without, 89 with).
+__device__ __forceinline__ long long row_at(int n) {
+  return static_cast<long long>(n) * gridDim.x + (blockIdx.x + 37ull * static_cast<unsigned>(n)) % gridDim.x;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(THREADS + 64, 2) k_distill(const DistillArgs A) {
   griddep_wait();
@@ -231,19 +251,17 @@ __global__ void __launch_bounds__(THREADS + 64, 2) k_distill(const DistillArgs A
   __shared__ float p_sh[MAX_TOP], part_sh[MAX_TOP];
   __shared__ int id_sh[MAX_TOP];
   __shared__ uint64_t full[SLOTS], empty[SLOTS];
+  __shared__ uint64_t ended;      // the computing warps are through
   __shared__ int abort_s, err_s;
+  __shared__ int lost_s;          // which of its rows the block has lost, and those after it: a wait gave up
   volatile int* abort_flag = &abort_s;
   const int tid = threadIdx.x, lane = tid & 31;
-  // The block's n-th row.  Each round starts 37 blocks further on: rows of weight zero at a regular distance do not all
-  // fall to the same blocks (2048 x 50,001, every fourth row: 100 microseconds without, 89 with).
-  const unsigned blocks = gridDim.x;
-  auto row_at = [&](int n) {
-    return static_cast<long long>(n) * blocks + (blockIdx.x + 37ull * static_cast<unsigned>(n)) % blocks;
-  };
   if (tid == 0) {
     for (int i = 0; i < SLOTS; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], THREADS / 32);
     for (int i = 0; i < AHEAD; ++i) mbar_init(&rec_full[i], 1), mbar_init(&rec_empty[i], THREADS / 32 + 1);
+    mbar_init(&ended, THREADS / 32);
     abort_s = err_s = 0;
+    lost_s = NONE;
     fence_mbar_init();
   }
   __syncthreads();
@@ -276,9 +294,11 @@ __global__ void __launch_bounds__(THREADS + 64, 2) k_distill(const DistillArgs A
       t = warp_sum(t);
       if (wr == 0.f) t.s = 0.f;
       if (lane == 0) {
-        ok = mbar_wait(&rec_empty[n % AHEAD], ((n / AHEAD) & 1) ^ 1u, abort_flag, &err_s, 4, TIMEOUT_NS);
-        rec[n % AHEAD] = Record{t, wr};
-        mbar_arrive(&rec_full[n % AHEAD]);
+        ok = mbar_wait(&rec_empty[n % AHEAD], ((n / AHEAD) & 1) ^ 1u, abort_flag, &err_s, 4, A.timeout_ns);
+        if (ok) {
+          rec[n % AHEAD] = Record{t, wr};
+          mbar_arrive(&rec_full[n % AHEAD]);
+        }
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
     }
@@ -290,22 +310,24 @@ __global__ void __launch_bounds__(THREADS + 64, 2) k_distill(const DistillArgs A
     int pos = 0, n = 0;
     bool ok = true;
     for (long long row = blockIdx.x; ok && row < A.n; row = row_at(++n)) {
-      ok = warp_ok(mbar_wait(&rec_full[n % AHEAD], (n / AHEAD) & 1, abort_flag, &err_s, 5, TIMEOUT_NS));
+      ok = warp_ok(mbar_wait(&rec_full[n % AHEAD], (n / AHEAD) & 1, abort_flag, &err_s, 5, A.timeout_ns));
+      if (!ok) break;
       const bool some = rec[n % AHEAD].t.s != 0.f;
       __syncwarp();
       if (lane == 0) mbar_arrive(&rec_empty[n % AHEAD]);
-      if (!ok || !some) continue;
+      if (!some) continue;
       const T* z = static_cast<const T*>(A.z) + row * A.z_stride;
       const Row R = row_of(z, A.V, twice);
       const uint8_t* from = reinterpret_cast<const uint8_t*>(z + R.head);
       if (lane == 0) {
         for (int i = 0; ok && i < R.chunks + R.again; ++i, ++pos) {
           const int c = i < R.chunks ? i : i - R.chunks, sl = pos % SLOTS;
-          ok = mbar_wait(&empty[sl], ((pos / SLOTS) & 1) ^ 1u, abort_flag, &err_s, 1, TIMEOUT_NS);
+          ok = mbar_wait(&empty[sl], ((pos / SLOTS) & 1) ^ 1u, abort_flag, &err_s, 1, A.timeout_ns);
           if (!ok) break;
           const uint32_t bytes = min(SLOT_VECS, R.nvec - c * SLOT_VECS) * 16;
           mbar_arrive_expect_tx(&full[sl], bytes);
           const uint8_t* src = from + static_cast<long long>(c) * SLOT;
+          if (pos == A.drop) continue;
           // what will be read again stays in L2 if what will not leaves first
           if (i < R.again) bulk_load(ring + sl * SLOT, src, bytes, &full[sl]);
           else bulk_load_hint(ring + sl * SLOT, src, bytes, &full[sl], once);
@@ -313,13 +335,22 @@ __global__ void __launch_bounds__(THREADS + 64, 2) k_distill(const DistillArgs A
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
     }
-    if (lane == 0 && (!ok || *abort_flag)) {
-      // bounded: no copy may still be writing shared memory when the block ends
+    if (lane == 0) {
+      // bounded: no copy may still be writing shared memory when the block ends, whoever gave up
       volatile int no_abort = 0;
       for (int q = pos > SLOTS ? pos - SLOTS : 0; q < pos; ++q)
-        mbar_wait(&full[q % SLOTS], (q / SLOTS) & 1, &no_abort, &err_s, 2, TIMEOUT_NS);
+        mbar_wait(&full[q % SLOTS], (q / SLOTS) & 1, &no_abort, &err_s, 2, A.timeout_ns);
+      // (a computing warp gives up once at most, and its row is bounded; no_abort is set where a copy is missing)
+      no_abort = 0;
+      if (!mbar_wait(&ended, 0, &no_abort, &err_s, 6, 4 * A.timeout_ns)) lost_s = 0;
     }
     __syncwarp();
+    const float nan = __int_as_float(0x7fffffff);
+    for (n = lost_s; n != NONE && (n == 0 || row_at(n) < A.n); ++n) {
+      if (lane == 0) A.loss[row_at(n)] = nan;
+      if (A.dz)
+        for (long long i = lane; i < A.V; i += 32) (static_cast<T*>(A.dz) + row_at(n) * A.dz_stride)[i] = W::round(nan);
+    }
     return;
   }
 
@@ -330,11 +361,9 @@ __global__ void __launch_bounds__(THREADS + 64, 2) k_distill(const DistillArgs A
     return e;
   };
   int pos = 0, n = 0;
-  bool good = true;      // no wait has given up
   auto slot_at = [&](int p) { return reinterpret_cast<const uint4*>(ring + p % SLOTS * SLOT); };
-  auto arrived = [&](uint64_t* bar, int parity) {
-    if (good && !mbar_wait(bar, parity, abort_flag, &err_s, 3, TIMEOUT_NS)) good = false;
-  };
+  // (one that gives up raises the abort flag, which is looked at once a row)
+  auto arrived = [&](uint64_t* bar, int parity) { mbar_wait(bar, parity, abort_flag, &err_s, 3, A.timeout_ns); };
   auto release = [&](int p) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[p % SLOTS]);
@@ -351,6 +380,8 @@ __global__ void __launch_bounds__(THREADS + 64, 2) k_distill(const DistillArgs A
     const int edge = tid < R.head ? tid : (tid >= 32 && tid - 32 < A.V - R.tail0 ? R.tail0 + tid - 32 : -1);
 
     arrived(&rec_full[n % AHEAD], (n / AHEAD) & 1);
+    // (also: the row before is done with the shared arrays)
+    if (any_thread(*abort_flag)) break;
     const Record known = rec[n % AHEAD];
     __syncwarp();
     if (lane == 0) mbar_arrive(&rec_empty[n % AHEAD]);
@@ -370,7 +401,7 @@ __global__ void __launch_bounds__(THREADS + 64, 2) k_distill(const DistillArgs A
           for (int i = tid; i < A.V; i += THREADS) dz[i] = W::round(0.f);
         }
       }
-      if (tid == 0) A.loss[row] = good && !*abort_flag ? 0.f : __int_as_float(0x7fffffff);
+      if (tid == 0) A.loss[row] = 0.f;
       continue;
     }
     const float zk = mine.id >= 0 ? W::one(z[mine.id]) : 0.f;
@@ -454,7 +485,7 @@ __global__ void __launch_bounds__(THREADS + 64, 2) k_distill(const DistillArgs A
     // the gradient is written and the entries are in shared memory
     sync_threads();
     if (tid < 32) {
-      float t = good && !*abort_flag ? 0.f : __int_as_float(0x7fffffff);
+      float t = 0.f;
       for (int k = tid; k < A.K; k += 32) t += part_sh[k];
 #pragma unroll
       for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
@@ -471,7 +502,12 @@ __global__ void __launch_bounds__(THREADS + 64, 2) k_distill(const DistillArgs A
         }
       if (first) dz[mine.id] = W::round(fmaf(-g, sum, __fmul_rn(inv, ex2(fmaf(zk, A.k2, -r.r)))));
     }
-    sync_threads();      // the shared arrays are reused for the next row
+  }
+  // the row before this one may be what a wait gave up in; none after it has been looked at
+  __syncwarp();
+  if (lane == 0) {
+    if (*abort_flag) atomicMin(&lost_s, max(n - 1, 0));
+    mbar_arrive(&ended);
   }
 }
 
@@ -500,6 +536,8 @@ extern "C" mlora_status mlora_distill_loss(const mlora_distill_problem* p, const
     return op_fail(MLORA_ERR_INVALID, "rows of the logits or of their gradient overlap");
   if (!(p->temperature > 0.f) || !(p->temperature < INFINITY))
     return op_fail(MLORA_ERR_INVALID, "the temperature must be positive and finite");
+  if (p->flags & ~(MLORA_DEBUG_SHORT_TIMEOUT | MLORA_DEBUG_DROP_COPY))
+    return op_fail(MLORA_ERR_INVALID, "unknown flag");
   if (!logits || !ids || !teacher || !loss) return op_fail(MLORA_ERR_INVALID, "null tensor argument");
   const unsigned es = p->dtype == MLORA_F32 ? 4 : 2;
   if (!ptr_aligned(logits, es) || !ptr_aligned(dlogits, es) || !ptr_aligned(ids, 4) || !ptr_aligned(teacher, 4) ||
@@ -509,7 +547,9 @@ extern "C" mlora_status mlora_distill_loss(const mlora_distill_problem* p, const
   cudaError_t e = device_sms(&sms);
   if (e != cudaSuccess) return op_cuda_fail(e, "querying the device");
   DistillArgs A{logits, ids, teacher, weight, loss, dlogits, p->n_tokens, p->logits_stride, p->dlogits_stride,
-                p->vocab, p->top, p->temperature, static_cast<float>(1.4426950408889634 / p->temperature), 0};
+                p->vocab, p->top, p->temperature, static_cast<float>(1.4426950408889634 / p->temperature), 0, 0,
+                p->flags & MLORA_DEBUG_SHORT_TIMEOUT ? 1000000ull : 4000000000ull};
+  A.drop = (p->flags & MLORA_DEBUG_SHORT_TIMEOUT) && (p->flags & MLORA_DEBUG_DROP_COPY) ? 2 : -1;
   A.same_align = (reinterpret_cast<uintptr_t>(logits) - reinterpret_cast<uintptr_t>(dlogits)) % 16 == 0 &&
                  (p->logits_stride - p->dlogits_stride) * es % 16 == 0;
   const long long most = static_cast<long long>(sms) * 2;

@@ -522,10 +522,13 @@ typedef struct mlora_distill_problem {
     float temperature;        /* > 0 */
     int64_t logits_stride;    /* elements between rows, at least vocab */
     int64_t dlogits_stride;
+    uint32_t flags;           /* MLORA_DEBUG_SHORT_TIMEOUT; with it MLORA_DEBUG_DROP_COPY: every block arms
+                                 its third slot and copies nothing into it */
 } mlora_distill_problem;
 
 /* ids int32 [n_tokens, top], teacher fp32 [n_tokens, top], weight and loss fp32 [n_tokens]; dlogits
- * may be NULL (loss alone).  Rows need no alignment beyond their elements'. */
+ * may be NULL (loss alone).  Rows need no alignment beyond their elements'.  Should a wait inside the kernel give up,
+ * the rows that it may concern get a loss and a gradient of NaN. */
 mlora_status mlora_distill_loss(const mlora_distill_problem* problem, const void* logits, const int32_t* ids,
                                 const float* teacher, const float* weight, float* loss, void* dlogits,
                                 void* stream);
