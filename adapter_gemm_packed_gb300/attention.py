@@ -196,12 +196,22 @@ class WindowAttention:
     def _new_saved(self):
         return torch.empty(self.saved_elems, dtype=torch.float32, device=self.device)
 
+    def _saved_ptr(self, t, where):
+        """The statistics' buffer: the object's own, or the caller's, of ``saved_elems`` floats."""
+        if t is None:
+            t = self.saved
+        elif not (t.dtype is torch.float32 and t.is_cuda and t.is_contiguous() and t.numel() >= self.saved_elems):
+            _refuse(where, f"saved must be a contiguous fp32 tensor of {self.saved_elems} elements on the GPU")
+        return None if t is None else t.data_ptr()
+
     def forward(self, q, k, v, out=None, stream=None, saved=None):
+        """Outputs [n_tokens, n_q_heads, head_dim].  ``saved`` (fp32, ``saved_elems`` elements) takes the
+        statistics instead of ``self.saved``; the backward is given the same buffer."""
         w = "WindowAttention.forward"
         a = (_heads(q, w, "q", *self.qs), _heads(k, w, "k", *self.ks), _heads(v, w, "v", *self.ks))
         with _on(stream) as s:
             out, o = _output(out, self.device, w, "out", *self.qs)
-            M.mlora_attention_forward(self.plan, *a, o, (self.saved if saved is None else saved).data_ptr(), s)
+            M.mlora_attention_forward(self.plan, *a, o, self._saved_ptr(saved, w), s)
         return out
 
     def backward(self, q, k, v, out, dout, dq=None, dk=None, dv=None, stream=None, saved=None):
@@ -213,8 +223,7 @@ class WindowAttention:
             dq, oq = _output(dq, self.device, w, "dq", *self.qs)
             dk, ok = _output(dk, self.device, w, "dk", *self.ks)
             dv, ov = _output(dv, self.device, w, "dv", *self.ks)
-            M.mlora_attention_backward(self.plan, *a, (self.saved if saved is None else saved).data_ptr(), oq, ok, ov,
-                                       s)
+            M.mlora_attention_backward(self.plan, *a, self._saved_ptr(saved, w), oq, ok, ov, s)
         return dq, dk, dv
 
     def __call__(self, q, k, v):

@@ -103,3 +103,27 @@ def test_delta_is_not_biased():
         want = (mean[:, 0] * torch.sign(o[:, h].double().cpu())).sum()
         assert abs(float(_delta(attn, [900], h).sum() - want)) <= 2.0 ** -19 * float(want)
     attn.close()
+
+
+# ------------------------------------------------------------------ arguments
+
+def test_buffers_for_the_statistics():
+    """A buffer of the caller's gives what the object's own gives; one that the kernels would write past the end of, or
+    in another type, is refused before anything runs."""
+    from adapter_gemm_packed_gb300.attention import WindowAttention
+    attn = WindowAttention([70, 40], 4, 2, 64, 30, n_sink=1)
+    q, k, v, do = (_draw((attn.n, h, 64), i, torch.bfloat16) for i, h in enumerate((4, 2, 2, 4)))
+    o = attn.forward(q, k, v)
+    want = (o, *attn.backward(q, k, v, o, do))
+    n = attn.saved_elems
+    mine = torch.empty(n, device="cuda")
+    o = attn.forward(q, k, v, saved=mine)
+    got = (o, *attn.backward(q, k, v, o, do, saved=mine))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for bad in (torch.empty(n - 1, device="cuda"), torch.empty(n, dtype=torch.bfloat16, device="cuda"), torch.empty(n),
+                torch.empty(2 * n, device="cuda")[::2], torch.empty(n + 1, device="cuda")[1:]):
+        for call in (lambda: attn.forward(q, k, v, saved=bad), lambda: attn.backward(q, k, v, o, do, saved=bad)):
+            with pytest.raises(M.MloraError) as e:
+                call()
+            assert e.value.status == M.MLORA_ERR_INVALID
+    attn.close()
