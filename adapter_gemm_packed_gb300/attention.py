@@ -8,6 +8,8 @@ in the library's kernels.  Outputs that are not given are allocated; with ``stre
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import _mlora as M
@@ -18,10 +20,15 @@ def _refuse(where: str, text: str, status: int = M.MLORA_ERR_INVALID):
     raise M.MloraError(status, where, text)
 
 
-def _heads(t, where: str, name: str, n: int, h: int, d: int, dt) -> M.mlora_heads:
-    """The C descriptor of a [n, h, d] tensor."""
-    if t.dtype is not dt or not t.is_cuda:
-        _refuse(where, f"{name} must be a {dt} tensor on the GPU, got {t.dtype} on {t.device}")
+def _launch_device(stream) -> int:
+    """Index of the device that a call's kernels run on: the stream's, or the current one."""
+    return torch._C._cuda_getDevice() if stream is None else stream.device.index
+
+
+def _heads(t, where: str, name: str, n: int, h: int, d: int, dt, dev: int) -> M.mlora_heads:
+    """The C descriptor of a [n, h, d] tensor on device ``dev``."""
+    if t.dtype is not dt or t.get_device() != dev:
+        _refuse(where, f"{name} must be a {dt} tensor on GPU {dev}, got {t.dtype} on {t.device}")
     if t.shape != (n, h, d):
         _refuse(where, f"{name} must be of shape {(n, h, d)}, got {tuple(t.shape)}")
     s = t.stride()
@@ -30,17 +37,18 @@ def _heads(t, where: str, name: str, n: int, h: int, d: int, dt) -> M.mlora_head
     return M.mlora_heads(t.data_ptr(), s[0], s[1])
 
 
-def _output(t, device, where: str, name: str, n: int, h: int, d: int, dt):
+def _output(t, where: str, name: str, n: int, h: int, d: int, dt, dev: int):
     """An output: the caller's, or a new one where that is None; and its C descriptor."""
     if t is not None:
-        return t, _heads(t, where, name, n, h, d, dt)
-    t = torch.empty((n, h, d), dtype=dt, device=device)
+        return t, _heads(t, where, name, n, h, d, dt, dev)
+    t = torch.empty((n, h, d), dtype=dt, device=dev)
     return t, M.mlora_heads(t.data_ptr(), h * d, d)
 
 
-def _vector(t, where: str, name: str, shape, dt) -> int:
-    if t.dtype is not dt or not t.is_cuda or t.shape != shape or not t.is_contiguous():
-        _refuse(where, f"{name} must be a contiguous {dt} tensor of shape {tuple(shape)} on the GPU")
+def _vector(t, where: str, name: str, shape, dt, dev: int) -> int:
+    if t.dtype is not dt or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        _refuse(where, f"{name} must be a contiguous {dt} tensor of shape {tuple(shape)} on GPU {dev}, "
+                       f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
@@ -63,7 +71,7 @@ class _on:
 
 # ------------------------------------------------------------------ norms with rotation
 
-def _rope_problem(where, q, k, wq, wk, cos, sin, positions, eps, interleaved):
+def _rope_problem(where, q, k, wq, wk, cos, sin, positions, eps, interleaved, dev):
     if q.dim() != 3 or k.dim() != 3:
         _refuse(where, "q and k must be [n_tokens, n_heads, head_dim]")
     n, hq, d = q.shape
@@ -79,10 +87,10 @@ def _rope_problem(where, q, k, wq, wk, cos, sin, positions, eps, interleaved):
     rows, half = cos.shape
     p = M.mlora_rope_problem(n, hq, hk, d, 2 * half, rows, code, M.MLORA_ROPE_INTERLEAVED if interleaved else 0, eps)
     f32 = torch.float32
-    tables = (_vector(wq, where, "wq", (d,), f32), _vector(wk, where, "wk", (d,), f32),
-              _vector(cos, where, "cos", (rows, half), f32), _vector(sin, where, "sin", (rows, half), f32),
-              _vector(positions, where, "positions", (n,), torch.int32))
-    return p, (n, hq, d, dt), (n, hk, d, dt), tables
+    tables = (_vector(wq, where, "wq", (d,), f32, dev), _vector(wk, where, "wk", (d,), f32, dev),
+              _vector(cos, where, "cos", (rows, half), f32, dev), _vector(sin, where, "sin", (rows, half), f32, dev),
+              _vector(positions, where, "positions", (n,), torch.int32, dev))
+    return p, (n, hq, d, dt, dev), (n, hk, d, dt, dev), tables
 
 
 def qk_norm_rope(q, k, wq, wk, cos, sin, positions, *, eps=1e-6, interleaved=False, q_out=None, k_out=None,
@@ -92,11 +100,12 @@ def qk_norm_rope(q, k, wq, wk, cos, sin, positions, *, eps=1e-6, interleaved=Fal
     ``cos`` / ``sin`` (fp32 [positions, rot_dim / 2]) hold for the token's position (int32
     [n_tokens]).  Returns (q_out, k_out)."""
     where = "qk_norm_rope"
-    p, sq, sk, tables = _rope_problem(where, q, k, wq, wk, cos, sin, positions, eps, interleaved)
+    p, sq, sk, tables = _rope_problem(where, q, k, wq, wk, cos, sin, positions, eps, interleaved,
+                                      _launch_device(stream))
     hq, hk = _heads(q, where, "q", *sq), _heads(k, where, "k", *sk)
     with _on(stream) as s:
-        q_out, oq = _output(q_out, q.device, where, "q_out", *sq)
-        k_out, ok = _output(k_out, q.device, where, "k_out", *sk)
+        q_out, oq = _output(q_out, where, "q_out", *sq)
+        k_out, ok = _output(k_out, where, "k_out", *sk)
         M.mlora_qk_norm_rope(p, hq, hk, *tables, oq, ok, s)
     return q_out, k_out
 
@@ -106,12 +115,13 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, wq, wk, cos, sin, positions, *, 
     """Gradients of :func:`qk_norm_rope` from those of its outputs and from its inputs.  Returns
     (dq, dk, dwq, dwk); the weights' gradients are None with ``weight_grads=False`` (frozen norms)."""
     where = "qk_norm_rope_backward"
-    p, sq, sk, tables = _rope_problem(where, q, k, wq, wk, cos, sin, positions, eps, interleaved)
+    p, sq, sk, tables = _rope_problem(where, q, k, wq, wk, cos, sin, positions, eps, interleaved,
+                                      _launch_device(stream))
     args = (_heads(dq_out, where, "dq_out", *sq), _heads(dk_out, where, "dk_out", *sk), _heads(q, where, "q", *sq),
             _heads(k, where, "k", *sk))
     with _on(stream) as s:
-        dq, oq = _output(dq, q.device, where, "dq", *sq)
-        dk, ok = _output(dk, q.device, where, "dk", *sk)
+        dq, oq = _output(dq, where, "dq", *sq)
+        dk, ok = _output(dk, where, "dk", *sk)
         dwq = dwk = ws = None
         if weight_grads:
             dwq = torch.empty(sq[2], dtype=torch.float32, device=q.device)
@@ -182,16 +192,23 @@ class WindowAttention:
         if n_tokens is None:
             n_tokens = max((s + n for s, n in zip(starts, lens)), default=0)
         code, self.tdtype = _DT[dtype]
+        host = flags & M.MLORA_PLAN_HOST_ONLY
         self.device = torch.device(device)
+        if not host:      # the plan's tables go where the tensors are
+            if self.device.type != "cuda":
+                _refuse("WindowAttention", f"the device must be a GPU, not {device}")
+            dev = torch.cuda.current_device() if self.device.index is None else self.device.index
+            self.device = torch.device("cuda", dev)
         self.n, self.hq, self.hk, self.d = int(n_tokens), int(n_q_heads), int(n_kv_heads), int(head_dim)
         self.scale = self.d ** -0.5 if scale is None else float(scale)
         self.plan = None
         p = M.mlora_attention_problem(self.n, self.hq, self.hk, self.d, min(int(window), 2**31 - 1),
                                       min(int(n_sink), 2**31 - 1), code, self.scale, flags)
-        self.plan = M.mlora_attention_plan(p, starts, lens)
+        with contextlib.nullcontext() if host else torch.cuda.device(self.device):
+            self.plan = M.mlora_attention_plan(p, starts, lens)
         self.saved_elems = max(4, M.mlora_attention_saved_elems(self.plan))
-        self.saved = None if flags & M.MLORA_PLAN_HOST_ONLY else self._new_saved()
-        self.qs, self.ks = (self.n, self.hq, self.d, self.tdtype), (self.n, self.hk, self.d, self.tdtype)
+        self.saved = None if host else self._new_saved()
+        self.qs, self.ks = ((self.n, h, self.d, self.tdtype, self.device.index) for h in (self.hq, self.hk))
 
     def _new_saved(self):
         return torch.empty(self.saved_elems, dtype=torch.float32, device=self.device)
@@ -200,8 +217,9 @@ class WindowAttention:
         """The statistics' buffer: the object's own, or the caller's, of ``saved_elems`` floats."""
         if t is None:
             t = self.saved
-        elif not (t.dtype is torch.float32 and t.is_cuda and t.is_contiguous() and t.numel() >= self.saved_elems):
-            _refuse(where, f"saved must be a contiguous fp32 tensor of {self.saved_elems} elements on the GPU")
+        elif not (t.dtype is torch.float32 and t.device == self.device and t.is_contiguous()
+                  and t.numel() >= self.saved_elems):
+            _refuse(where, f"saved must be a contiguous fp32 tensor of {self.saved_elems} elements on {self.device}")
         return None if t is None else t.data_ptr()
 
     def forward(self, q, k, v, out=None, stream=None, saved=None):
@@ -210,7 +228,7 @@ class WindowAttention:
         w = "WindowAttention.forward"
         a = (_heads(q, w, "q", *self.qs), _heads(k, w, "k", *self.ks), _heads(v, w, "v", *self.ks))
         with _on(stream) as s:
-            out, o = _output(out, self.device, w, "out", *self.qs)
+            out, o = _output(out, w, "out", *self.qs)
             M.mlora_attention_forward(self.plan, *a, o, self._saved_ptr(saved, w), s)
         return out
 
@@ -220,9 +238,9 @@ class WindowAttention:
         a = (_heads(q, w, "q", *self.qs), _heads(k, w, "k", *self.ks), _heads(v, w, "v", *self.ks),
              _heads(out, w, "out", *self.qs), _heads(dout, w, "dout", *self.qs))
         with _on(stream) as s:
-            dq, oq = _output(dq, self.device, w, "dq", *self.qs)
-            dk, ok = _output(dk, self.device, w, "dk", *self.ks)
-            dv, ov = _output(dv, self.device, w, "dv", *self.ks)
+            dq, oq = _output(dq, w, "dq", *self.qs)
+            dk, ok = _output(dk, w, "dk", *self.ks)
+            dv, ov = _output(dv, w, "dv", *self.ks)
             M.mlora_attention_backward(self.plan, *a, self._saved_ptr(saved, w), oq, ok, ov, s)
         return dq, dk, dv
 

@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import torch
 
-from .attention import WindowAttention, qk_norm_rope, qk_norm_rope_backward
+from .attention import WindowAttention, _launch_device, _refuse, qk_norm_rope, qk_norm_rope_backward
 from .distill import distill_loss
 from .layer import PackedLoRA
 
@@ -25,6 +25,8 @@ class DistilledAttention:
         self.Wqkv, self.Wo, self.Wh = Wqkv, Wo, Wh
         self.hq, self.hk, self.d, self.eps = n_q_heads, n_kv_heads, head_dim, eps
         dev, d_model, vocab = Wqkv.device, Wqkv.shape[1], Wh.shape[0]
+        if any(w.get_device() != _launch_device(None) for w in (Wqkv, Wo, Wh)):
+            _refuse("DistilledAttention", "the weights must be on the current GPU, where the packs' plans are built")
         tokens = [sum(s) for s in samples]
         lens = [n for s in samples for n in s]
         widths = [n_q_heads * head_dim, n_kv_heads * head_dim, n_kv_heads * head_dim]

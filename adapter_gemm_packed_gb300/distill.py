@@ -4,7 +4,7 @@ from __future__ import annotations
 import torch
 
 from . import _mlora as M
-from .attention import _on, _refuse, _vector
+from .attention import _launch_device, _on, _refuse, _vector
 
 
 def distill_loss(logits, ids, teacher, weight=None, *, temperature=1.0, grad=True, dlogits=None, stream=None):
@@ -18,8 +18,9 @@ def distill_loss(logits, ids, teacher, weight=None, *, temperature=1.0, grad=Tru
     which ``logits.backward(dlogits)`` hands on; None with ``grad=False``.  Rows of weight zero have loss
     and gradient zero."""
     where = "distill_loss"
-    if logits.dim() != 2 or not logits.is_cuda or (logits.shape[1] > 1 and logits.stride(1) != 1):
-        _refuse(where, "logits must be [n_tokens, vocab] on the GPU with contiguous rows")
+    dev = _launch_device(stream)
+    if logits.dim() != 2 or logits.get_device() != dev or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        _refuse(where, f"logits must be [n_tokens, vocab] on GPU {dev} with contiguous rows")
     if logits.dtype is torch.bfloat16:
         code = M.MLORA_BF16
     elif logits.dtype is torch.float32:
@@ -30,17 +31,18 @@ def distill_loss(logits, ids, teacher, weight=None, *, temperature=1.0, grad=Tru
     if ids.dim() != 2:
         _refuse(where, "ids must be [n_tokens, top]")
     top = ids.shape[1]
-    a = (_vector(ids, where, "ids", (n, top), torch.int32), _vector(teacher, where, "teacher", (n, top), torch.float32),
-         None if weight is None else _vector(weight, where, "weight", (n,), torch.float32))
+    a = (_vector(ids, where, "ids", (n, top), torch.int32, dev),
+         _vector(teacher, where, "teacher", (n, top), torch.float32, dev),
+         None if weight is None else _vector(weight, where, "weight", (n,), torch.float32, dev))
     with _on(stream) as s:
         loss = torch.empty(n, dtype=torch.float32, device=logits.device)
         if not grad:
             dlogits = None
         elif dlogits is None:
             dlogits = torch.empty((n, v), dtype=logits.dtype, device=logits.device)
-        elif (dlogits.dtype is not logits.dtype or not dlogits.is_cuda or dlogits.shape != logits.shape
+        elif (dlogits.dtype is not logits.dtype or dlogits.get_device() != dev or dlogits.shape != logits.shape
               or (v > 1 and dlogits.stride(1) != 1)):
-            _refuse(where, "dlogits must be of the logits' type and shape, with contiguous rows")
+            _refuse(where, "dlogits must be of the logits' type, shape and device, with contiguous rows")
         # a single row has no stride to keep to
         p = M.mlora_distill_problem(n, v, top, code, temperature, logits.stride(0) if n > 1 else v,
                                     v if dlogits is None or n == 1 else dlogits.stride(0))
