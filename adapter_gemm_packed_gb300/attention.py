@@ -11,6 +11,7 @@ from __future__ import annotations
 import contextlib
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _mlora as M
 from .layer import _DT
@@ -140,6 +141,7 @@ class _NormRopeFn(torch.autograd.Function):
         return qk_norm_rope(q, k, wq, wk, cos, sin, positions, **ctx.opt)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq_out, dk_out):
         need = ctx.needs_input_grad[2] or ctx.needs_input_grad[3]
         dq, dk, dwq, dwk = qk_norm_rope_backward(dq_out.contiguous(), dk_out.contiguous(), *ctx.saved_tensors,
@@ -273,6 +275,7 @@ class _AttentionFn(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         q, k, v, out, saved = ctx.saved_tensors
         return (*ctx.attn.backward(q, k, v, out, dout.contiguous(), saved=saved), None)

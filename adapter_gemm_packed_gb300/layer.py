@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes as C
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _mlora as M
 
@@ -200,6 +201,7 @@ class _PackedLoRAFn(torch.autograd.Function):
         return layer.forward(X, Wt)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dY):
         (X,) = ctx.saved_tensors
         dX = ctx.layer.backward(X, ctx.Wt, dY.contiguous())

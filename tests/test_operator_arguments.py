@@ -65,3 +65,29 @@ def test_attention_takes_tensors_of_its_plans_device():
     _refused(lambda: attn.backward(ok, ok, ok, ok, bad))
     _refused(lambda: A.WindowAttention([6], 2, 2, 64, 4, device="cpu"))
     attn.close()
+
+
+def _twice(fn, x, *args):
+    """A second derivative through a function whose first is the library's: an error, not a constant's."""
+    y = fn.apply(*args)
+    y = y[0] if isinstance(y, tuple) else y
+    (g,) = torch.autograd.grad(y.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.sum().backward()
+
+
+def test_second_derivatives_are_refused(monkeypatch):
+    from adapter_gemm_packed_gb300 import layer as L
+    x = lambda *s: torch.randn(s, requires_grad=True)
+    attn = SimpleNamespace(_new_saved=lambda: torch.zeros(4), forward=lambda q, k, v, saved: q + k + v,
+                           backward=lambda q, k, v, o, do, saved: (do * o, do * o, do * o))
+    q, k, v = x(3, 2, 8), x(3, 2, 8), x(3, 2, 8)
+    _twice(A._AttentionFn, q, q, k, v, attn)
+    monkeypatch.setattr(A, "qk_norm_rope", lambda q, k, *t, **kw: (2 * q, 2 * k))
+    monkeypatch.setattr(A, "qk_norm_rope_backward",
+                        lambda dq, dk, q, k, *t, weight_grads, **kw: (2 * dq * q, 2 * dk * k, None, None))
+    w = torch.ones(8)
+    _twice(A._NormRopeFn, q, q, k, w, w, w, w, w, 1e-6, False)
+    layer = SimpleNamespace(forward=lambda X, W: X @ W, backward=lambda X, W, dY: dY @ W.T * X)
+    X = x(3, 4)
+    _twice(L._PackedLoRAFn, X, X, layer, torch.ones(4, 5))
