@@ -136,19 +136,16 @@ __device__ __forceinline__ float group_sum(float v) {
 
 template <int R>
 __device__ __forceinline__ void load_table(const RopeArgs& A, const Lane& ln, int pos, float (&c)[R], float (&s)[R]) {
-  if (ln.ci >= 0) {
-    // a position outside of the tables gives NaN, never a read outside of them
-    if (pos >= 0 && pos < A.max_pos) {
-      const long long at = static_cast<long long>(pos) * (A.rot / 2) + ln.ci;
-      load_f32(A.cos + at, c);
-      load_f32(A.sin + at, s);
-    } else {
-#pragma unroll
-      for (int i = 0; i < R; ++i) c[i] = s[i] = __int_as_float(0x7fffffff);
-    }
+  // a position outside of the tables gives NaN in the whole head vector, never a read outside of them
+  const bool ok = static_cast<unsigned>(pos) < static_cast<unsigned>(A.max_pos);
+  if (ok && ln.ci >= 0) {
+    const long long at = static_cast<long long>(pos) * (A.rot / 2) + ln.ci;
+    load_f32(A.cos + at, c);
+    load_f32(A.sin + at, s);
   } else {
+    const float nan = __int_as_float(0x7fffffff);
 #pragma unroll
-    for (int i = 0; i < R; ++i) c[i] = 1.f, s[i] = 0.f;
+    for (int i = 0; i < R; ++i) c[i] = ok ? 1.f : nan, s[i] = ok ? 0.f : nan;
   }
 }
 

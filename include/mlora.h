@@ -429,7 +429,8 @@ typedef struct mlora_rope_problem {
 } mlora_rope_problem;
 
 /* wq, wk: fp32 [head_dim]; cos_table, sin_table: fp32 [max_pos, rot_dim / 2] (16-byte aligned);
- * positions: int32 [n_tokens] in [0, max_pos); a token whose position lies outside gets NaN outputs.
+ * positions: int32 [n_tokens] in [0, max_pos); a token whose position lies outside gets NaN in every element
+ * of its outputs, and of its dq and dk (the weight gradients, which it is part of, are NaN then too).
  * Arithmetic is fp32, outputs are rounded once. */
 mlora_status mlora_qk_norm_rope(const mlora_rope_problem* problem, const mlora_heads* q, const mlora_heads* k,
                                 const float* wq, const float* wk, const float* cos_table, const float* sin_table,

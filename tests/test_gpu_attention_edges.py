@@ -127,3 +127,30 @@ def test_buffers_for_the_statistics():
                 call()
             assert e.value.status == M.MLORA_ERR_INVALID
     attn.close()
+
+
+# ------------------------------------------------------------------ norms with rotation
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("d,rot", [(64, 16), (128, 64), (40, 24), (96, 96)])
+def test_positions_outside_the_tables_give_nan_in_every_element(d, rot, inter, dtype):
+    """Those that are not rotated as well, forward and backward; the other tokens are what they are without it."""
+    from adapter_gemm_packed_gb300.attention import qk_norm_rope, qk_norm_rope_backward
+    n, hq, hk = 9, 6, 2
+    q, k, dq, dk = (_draw((n, h, d), i, DT[dtype]) for i, h in enumerate((hq, hk, hq, hk)))
+    w = [1 + 0.1 * _draw((d,), 7 + i, torch.float32) for i in range(2)]
+    ang = torch.rand((50, rot // 2), generator=torch.Generator().manual_seed(1)) * 6.28
+    tab = (*w, ang.cos().cuda(), ang.sin().cuda())
+    good = torch.arange(n, dtype=torch.int32, device="cuda") * 5
+    call = lambda pos: (*qk_norm_rope(q, k, *tab, pos, interleaved=inter),
+                        *qk_norm_rope_backward(dq, dk, q, k, *tab, pos, interleaved=inter))
+    want = call(good)
+    pos = good.clone()
+    pos[1], pos[4], pos[8] = -1, 50, 2**31 - 1
+    got = call(pos)
+    bad = torch.zeros(n, dtype=torch.bool, device="cuda")
+    bad[[1, 4, 8]] = True
+    for a, b in zip(got[:4], want[:4]):
+        assert a[bad].isnan().all() and torch.equal(a[~bad], b[~bad])
+    assert got[4].isnan().all() and got[5].isnan().all()
