@@ -53,6 +53,14 @@ def _vector(t, where: str, name: str, shape, dt, dev: int) -> int:
     return t.data_ptr()
 
 
+def _int32(where: str, name: str, v) -> int:
+    """A size for a 32-bit field of the C ABI, where a larger one would wrap around."""
+    v = int(v)
+    if not -2**31 <= v < 2**31:
+        _refuse(where, f"{name} = {v} does not fit in 32 bits")
+    return v
+
+
 class _on:
     """Run a call's allocations on the stream that its kernels use."""
 
@@ -86,6 +94,7 @@ def _rope_problem(where, q, k, wq, wk, cos, sin, positions, eps, interleaved, de
     if cos.dim() != 2:
         _refuse(where, "cos and sin must be [positions, rot_dim / 2]")
     rows, half = cos.shape
+    _int32(where, "the largest size", max(hq, hk, d, 2 * half, rows))
     p = M.mlora_rope_problem(n, hq, hk, d, 2 * half, rows, code, M.MLORA_ROPE_INTERLEAVED if interleaved else 0, eps)
     f32 = torch.float32
     tables = (_vector(wq, where, "wq", (d,), f32, dev), _vector(wk, where, "wk", (d,), f32, dev),
@@ -185,7 +194,8 @@ class WindowAttention:
                  n_tokens=None, device="cuda", flags=0):
         if dtype not in ("bf16", "f32"):
             _refuse("WindowAttention", f"queries, keys and values are bf16 or f32, not {dtype}", M.MLORA_ERR_UNSUPPORTED)
-        lens = [int(n) for n in lens]
+        here = "WindowAttention"
+        lens = [_int32(here, "a sequence's length", n) for n in lens]
         if starts is None:
             starts = [sum(lens[:i]) for i in range(len(lens))]
         starts = [int(s) for s in starts]
@@ -201,11 +211,15 @@ class WindowAttention:
                 _refuse("WindowAttention", f"the device must be a GPU, not {device}")
             dev = torch.cuda.current_device() if self.device.index is None else self.device.index
             self.device = torch.device("cuda", dev)
-        self.n, self.hq, self.hk, self.d = int(n_tokens), int(n_q_heads), int(n_kv_heads), int(head_dim)
+        self.n = int(n_tokens)
+        self.hq, self.hk = _int32(here, "n_q_heads", n_q_heads), _int32(here, "n_kv_heads", n_kv_heads)
+        self.d = _int32(here, "head_dim", head_dim)
         self.scale = self.d ** -0.5 if scale is None else float(scale)
         self.plan = None
-        p = M.mlora_attention_problem(self.n, self.hq, self.hk, self.d, min(int(window), 2**31 - 1),
-                                      min(int(n_sink), 2**31 - 1), code, self.scale, flags)
+        # (a window or a number of first tokens beyond every length is no different from a smaller one)
+        window, n_sink = (_int32(here, *x) for x in (("window", min(int(window), 2**31 - 1)),
+                                                     ("n_sink", min(int(n_sink), 2**31 - 1))))
+        p = M.mlora_attention_problem(self.n, self.hq, self.hk, self.d, window, n_sink, code, self.scale, flags)
         with contextlib.nullcontext() if host else torch.cuda.device(self.device):
             self.plan = M.mlora_attention_plan(p, starts, lens)
         self.saved_elems = max(4, M.mlora_attention_saved_elems(self.plan))

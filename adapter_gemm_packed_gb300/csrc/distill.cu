@@ -27,6 +27,8 @@
 //
 // Waits have a limit.  Whether one has given up is settled by the computing threads together at the start of every row, so
 // that they never part ways; a block's rows from there on, and the one before, get a loss and a gradient of NaN.
+#include <climits>
+
 #include "entry.cuh"
 
 namespace mlora {
@@ -531,6 +533,8 @@ extern "C" mlora_status mlora_distill_loss(const mlora_distill_problem* p, const
     return op_fail(MLORA_ERR_UNSUPPORTED, "logits are bf16 or fp32");
   if (p->n_tokens < 1 || p->vocab < 1 || p->top < 1)
     return op_fail(MLORA_ERR_INVALID, "tokens, vocabulary and teacher entries must be positive");
+  if (p->vocab > INT_MAX - 4096)      // places in a row, a step of all threads ahead, stay within 32 bits
+    return op_fail(MLORA_ERR_UNSUPPORTED, "vocabulary out of range");
   if (p->top > MAX_TOP) return op_fail(MLORA_ERR_UNSUPPORTED, "at most 256 teacher entries a row");
   if (p->logits_stride < p->vocab || (dlogits && p->dlogits_stride < p->vocab))
     return op_fail(MLORA_ERR_INVALID, "rows of the logits or of their gradient overlap");

@@ -4,7 +4,7 @@ from __future__ import annotations
 import torch
 
 from . import _mlora as M
-from .attention import _launch_device, _on, _refuse, _vector
+from .attention import _int32, _launch_device, _on, _refuse, _vector
 
 
 def distill_loss(logits, ids, teacher, weight=None, *, temperature=1.0, grad=True, dlogits=None, stream=None):
@@ -27,10 +27,10 @@ def distill_loss(logits, ids, teacher, weight=None, *, temperature=1.0, grad=Tru
         code = M.MLORA_F32
     else:
         _refuse(where, f"logits are bf16 or fp32, not {logits.dtype}", M.MLORA_ERR_UNSUPPORTED)
-    n, v = logits.shape
+    n, v = logits.shape[0], _int32(where, "vocab", logits.shape[1])
     if ids.dim() != 2:
         _refuse(where, "ids must be [n_tokens, top]")
-    top = ids.shape[1]
+    top = _int32(where, "top", ids.shape[1])
     a = (_vector(ids, where, "ids", (n, top), torch.int32, dev),
          _vector(teacher, where, "teacher", (n, top), torch.float32, dev),
          None if weight is None else _vector(weight, where, "weight", (n,), torch.float32, dev))

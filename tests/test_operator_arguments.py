@@ -91,3 +91,38 @@ def test_second_derivatives_are_refused(monkeypatch):
     layer = SimpleNamespace(forward=lambda X, W: X @ W, backward=lambda X, W, dY: dY @ W.T * X)
     X = x(3, 4)
     _twice(L._PackedLoRAFn, X, X, layer, torch.ones(4, 5))
+
+
+WRAP = 2**32
+
+
+@pytest.mark.parametrize("kw", [dict(lens=[WRAP + 6]), dict(n_q_heads=WRAP + 2), dict(n_kv_heads=WRAP + 2),
+                                dict(head_dim=WRAP + 64), dict(window=-WRAP + 4), dict(n_sink=-WRAP)])
+def test_sizes_that_32_bits_do_not_hold_are_refused(kw):
+    """They would come around to ordinary ones."""
+    args = dict(lens=[6], n_q_heads=2, n_kv_heads=2, head_dim=64, window=4, n_tokens=6, flags=M.MLORA_PLAN_HOST_ONLY)
+    A.WindowAttention(**args).close()
+    A.WindowAttention(**{**args, "window": 2**40, "n_sink": 2**40}).close()
+    _refused(lambda: A.WindowAttention(**{**args, **kw}))
+
+
+def test_a_vocabulary_that_32_bits_do_not_hold_is_refused(monkeypatch):
+    from adapter_gemm_packed_gb300.distill import distill_loss
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    z = _on_gpu(0, (1, 100))
+    z.shape, z.stride = torch.Size((1, WRAP + 100)), lambda *i: 1
+    _refused(lambda: distill_loss(z, _on_gpu(0, (1, 3), torch.int32), _on_gpu(0, (1, 3), torch.float32)))
+    p = M.mlora_distill_problem(1, 2**31 - 200, 3, M.MLORA_BF16, 1.0, 2**31, 2**31)
+    _refused(lambda: M.mlora_distill_loss(p, 16, 16, 16, None, 16, 16, None), M.MLORA_ERR_UNSUPPORTED)
+
+
+def test_norm_sizes_that_32_bits_do_not_hold_are_refused(monkeypatch):
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    w, half = _on_gpu(0, (64,), torch.float32), _on_gpu(0, (9, 32), torch.float32)
+    long = _on_gpu(0, (9, 32), torch.float32)
+    long.shape = torch.Size((WRAP + 9, 32))
+    q, many, pos = _on_gpu(0), _on_gpu(0), _on_gpu(0, (6,), torch.int32)
+    many.shape = torch.Size((6, WRAP + 2, 64))
+    _refused(lambda: A.qk_norm_rope(q, q, w, w, long, long, pos))
+    _refused(lambda: A.qk_norm_rope(many, q, w, w, half, half, pos))
+    _refused(lambda: A.qk_norm_rope(q, many, w, w, half, half, pos))
