@@ -61,6 +61,13 @@ def _int32(where: str, name: str, v) -> int:
     return v
 
 
+def _gradient(t):
+    """A gradient as autograd hands it over, laid out for the kernels: it may be a slice of a larger one, at any
+    element, or broadcast."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class _on:
     """Run a call's allocations on the stream that its kernels use."""
 
@@ -153,7 +160,7 @@ class _NormRopeFn(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dq_out, dk_out):
         need = ctx.needs_input_grad[2] or ctx.needs_input_grad[3]
-        dq, dk, dwq, dwk = qk_norm_rope_backward(dq_out.contiguous(), dk_out.contiguous(), *ctx.saved_tensors,
+        dq, dk, dwq, dwk = qk_norm_rope_backward(_gradient(dq_out), _gradient(dk_out), *ctx.saved_tensors,
                                                  weight_grads=need, **ctx.opt)
         return dq, dk, dwq, dwk, None, None, None, None, None
 
@@ -292,4 +299,4 @@ class _AttentionFn(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dout):
         q, k, v, out, saved = ctx.saved_tensors
-        return (*ctx.attn.backward(q, k, v, out, dout.contiguous(), saved=saved), None)
+        return (*ctx.attn.backward(q, k, v, out, _gradient(dout), saved=saved), None)

@@ -154,3 +154,35 @@ def test_positions_outside_the_tables_give_nan_in_every_element(d, rot, inter, d
     for a, b in zip(got[:4], want[:4]):
         assert a[bad].isnan().all() and torch.equal(a[~bad], b[~bad])
     assert got[4].isnan().all() and got[5].isnan().all()
+
+
+# ------------------------------------------------------------------ autograd
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gradients_that_start_anywhere(dtype):
+    """A gradient that is a slice of another starts at any element, a broadcast one has strides of zero: both give what a
+    tensor of its own gives."""
+    from adapter_gemm_packed_gb300.attention import QKNormRope, WindowAttention
+    n, hq, hk, d, dt = 40, 4, 2, 64, DT[dtype]
+    attn, norm = WindowAttention([n], hq, hk, d, 30, dtype=dtype), QKNormRope(d, 64)
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    g = _draw((n * hq * d + 3,), 5, dt)
+    leaves = lambda: [_draw((n, h, d), i, dt).requires_grad_() for i, h in enumerate((hq, hk, hk))]
+
+    def grads(use):
+        x = leaves()
+        use(x).backward()
+        return [t.grad for t in x[:2]]
+
+    both = lambda x: norm(x[0], x[1], pos)
+    kg = _draw((n, hk, d), 6, dt)
+    for one, other in [
+            (lambda x: (attn(*both(x), x[2]) * g[3:].view(n, hq, d)).sum(),
+             lambda x: (torch.cat([x[0].flatten()[:3].detach(), attn(*both(x), x[2]).flatten()]) * g).sum()),
+            (lambda x: (both(x)[0] * g[3:].view(n, hq, d)).sum() + (both(x)[1] * kg).sum(),
+             lambda x: (torch.cat([x[0].flatten()[:3].detach(), both(x)[0].flatten()]) * g).sum() + (both(x)[1] * kg).sum()),
+            (lambda x: (attn(*both(x), x[2]) * torch.ones((n, hq, d), dtype=dt, device="cuda")).sum(),
+             lambda x: attn(*both(x), x[2]).sum())]:
+        for a, b in zip(grads(one), grads(other)):
+            assert torch.equal(a, b)
+    attn.close()
