@@ -40,7 +40,8 @@ inline mlora_status check_heads(const mlora_heads* t, const char* name, int64_t 
     snprintf(buf, sizeof buf, "%s: null tensor argument", name);
     return op_fail(MLORA_ERR_INVALID, buf);
   }
-  const int64_t unit = 16 / esize, rs = t->row_stride, hs = t->head_stride;
+  // (the stride of a dimension with one element is never used, and views carry anything there)
+  const int64_t unit = 16 / esize, rs = n_tokens == 1 ? 0 : t->row_stride, hs = n_heads == 1 ? 0 : t->head_stride;
   if (!ptr_aligned(t->data, 16) || rs % unit || hs % unit) {
     snprintf(buf, sizeof buf, "%s: the base and both strides must be multiples of 16 bytes", name);
     return op_fail(MLORA_ERR_INVALID, buf);

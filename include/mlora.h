@@ -404,7 +404,7 @@ mlora_status mlora_forward_static_ws(const mlora_plan_t* plan, const void* X, co
 /* A [n_tokens, n_heads, head_dim] tensor in device memory whose head vectors are contiguous.  Base
  * and strides are multiples of 16 bytes and no two head vectors overlap: tokens or heads may be the
  * outer dimension, and the heads may be a part of wider rows, as the q, k and v columns of a
- * shared-input pack's Y (or dY) are. */
+ * shared-input pack's Y (or dY) are.  The stride of a dimension with one element is not looked at. */
 typedef struct mlora_heads {
     void* data;
     int64_t row_stride;    /* elements from one token to the next */

@@ -186,3 +186,32 @@ def test_gradients_that_start_anywhere(dtype):
         for a, b in zip(grads(one), grads(other)):
             assert torch.equal(a, b)
     attn.close()
+
+
+# ------------------------------------------------------------------ strides
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_strides_of_dimensions_of_one_element_are_not_looked_at(dtype):
+    """A view of one token, or of one head, may carry any stride there: here odd ones."""
+    from adapter_gemm_packed_gb300.attention import WindowAttention, qk_norm_rope, qk_norm_rope_backward
+    d, dt = 64, DT[dtype]
+    w = [1 + 0.1 * _draw((d,), 7 + i, torch.float32) for i in range(2)]
+    ang = torch.rand((300, d // 2), generator=torch.Generator().manual_seed(1)) * 6.28
+    for n, hq, hk in ((1, 4, 2), (1, 1, 1), (200, 1, 1), (1, 3, 1)):
+        pos = torch.arange(n, dtype=torch.int32, device="cuda")
+        tab = (*w, ang.cos().cuda(), ang.sin().cuda(), pos)
+        q, k, v, do = (_draw((n, h, d), i, dt) for i, h in enumerate((hq, hk, hk, hq)))
+        attn = WindowAttention([n], hq, hk, d, 50, n_sink=1, dtype=dtype)
+
+        def all_of(q, k, v, do, *out):
+            out = out or [None] * 4
+            r = [*qk_norm_rope(q, k, *tab), *qk_norm_rope_backward(do, v, q, k, *tab)]
+            o = attn.forward(q, k, v, out=out[0])
+            return r + [o, *attn.backward(q, k, v, o, do, *out[1:])]
+
+        odd = lambda t: t.as_strided(t.shape, [77 if n == 1 else t.stride(0), 33 if t.shape[1] == 1 else t.stride(1), 1])
+        want = all_of(q, k, v, do)
+        got = all_of(*map(odd, (q, k, v, do)), *(odd(torch.empty_like(t)) for t in (q, q, k, v)))
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert attn.sync_status() == M.MLORA_OK
+        attn.close()
