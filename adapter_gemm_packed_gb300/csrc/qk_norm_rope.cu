@@ -398,6 +398,7 @@ mlora_status check(const mlora_rope_problem* p) {
     return op_fail(MLORA_ERR_UNSUPPORTED, "head_dim must be a multiple of 8, at most 256");
   if (p->rot_dim < 8 || p->rot_dim > p->head_dim || p->rot_dim % 8)
     return op_fail(MLORA_ERR_UNSUPPORTED, "rot_dim must be a multiple of 8, at most head_dim");
+  if (p->flags & ~MLORA_ROPE_INTERLEAVED) return op_fail(MLORA_ERR_INVALID, "unknown flag");
   if (!(p->eps >= 0.f)) return op_fail(MLORA_ERR_INVALID, "eps must not be negative");
   return MLORA_OK;
 }

@@ -126,3 +126,16 @@ def test_norm_sizes_that_32_bits_do_not_hold_are_refused(monkeypatch):
     _refused(lambda: A.qk_norm_rope(q, q, w, w, long, long, pos))
     _refused(lambda: A.qk_norm_rope(many, q, w, w, half, half, pos))
     _refused(lambda: A.qk_norm_rope(q, many, w, w, half, half, pos))
+
+
+def test_unknown_flags_are_refused():
+    ptr, w = M.mlora_heads(4096, 128, 64), 4096
+    call = lambda f: M.mlora_qk_norm_rope(M.mlora_rope_problem(4, 2, 2, 64, 64, 16, M.MLORA_BF16, f, 1e-6), ptr, None, w, w, w,
+                                          w, w, ptr, ptr, None)
+    with pytest.raises(M.MloraError, match="unknown flag"):
+        call(2)
+    with pytest.raises(M.MloraError, match="k: null"):
+        call(M.MLORA_ROPE_INTERLEAVED)
+    p = M.mlora_distill_problem(1, 200, 3, M.MLORA_BF16, 1.0, 200, 200, 1 << 20)
+    with pytest.raises(M.MloraError, match="unknown flag"):
+        M.mlora_distill_loss(p, 16, 16, 16, None, 16, 16, None)
