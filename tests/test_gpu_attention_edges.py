@@ -215,3 +215,81 @@ def test_strides_of_dimensions_of_one_element_are_not_looked_at(dtype):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert attn.sync_status() == M.MLORA_OK
         attn.close()
+
+
+# ------------------------------------------------------------------ pieces cut along their queries
+
+CUT = {"causal": ([2600], 10**6, 0), "first_tokens": ([4200, 30], 200, 70), "wide": ([70, 3500, 1], 1500, 3)}
+
+
+def _parts(attn):
+    """The largest number of parts that a dK / dV piece of the plan is cut into."""
+    t = M.mlora_attention_describe(attn.plan, M.MLORA_ATTN_Q_KEYS)
+    return max(t[6::8])
+
+
+@pytest.mark.parametrize("name", sorted(CUT))
+@pytest.mark.parametrize("hq,hk,d", [(4, 1, 64), (4, 1, 128), (8, 2, 72)])
+def test_cut_pieces(name, hq, hk, d):
+    """dK and dV of long pieces are summed by several blocks: against 64 bits; the same bits in every backward on one
+    buffer (the counters are back at zero), in a graph's replay, and with the sequences inside a larger pack.  Tolerance as
+    for all bf16 attention: 2^-8 of the result and 2^-7 of the sum of absolute terms."""
+    from adapter_gemm_packed_gb300.attention import WindowAttention
+    lens, window, sinks = CUT[name]
+    attn = WindowAttention(lens, hq, hk, d, window, n_sink=sinks)
+    assert _parts(attn) > 1
+    q, k, v, do = (_draw((attn.n, h, d), 50 + i, torch.bfloat16) for i, h in enumerate((hq, hk, hk, hq)))
+    o = attn.forward(q, k, v)
+    first = attn.backward(q, k, v, o, do)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(attn.backward(q, k, v, o, do), first))
+    starts = [sum(lens[:i]) for i in range(len(lens))]
+    ref = R.attention(q, k, v, lens, starts, window, sinks, attn.scale, do)
+    for what, got in zip(("o", "dq", "dk", "dv"), (o, *first)):
+        want, bound = ref[what]
+        err = (got.double().cpu() - want).abs()
+        assert (err <= 2.0 ** -8 * want.abs() + 2.0 ** -7 * bound + 1e-30).all(), what
+
+    out = [torch.empty_like(t) for t in (o, *first)]
+    step = lambda: (attn.forward(q, k, v, out=out[0]), attn.backward(q, k, v, out[0], do, *out[1:]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(2):
+        for t in out:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, (o, *first)))
+
+    # behind other sequences, which are cut too, and before others
+    others, after = [1000, 2900], [333]
+    big = WindowAttention(others + lens + after, hq, hk, d, window, n_sink=sinks)
+    pad = lambda t, s: torch.cat([_draw((sum(others), *t.shape[1:]), s, t.dtype), t, _draw((333, *t.shape[1:]), s + 1, t.dtype)])
+    Q, K, V, G = (pad(t, 60 + 2 * i) for i, t in enumerate((q, k, v, do)))
+    O = big.forward(Q, K, V)
+    inside = slice(sum(others), sum(others) + attn.n)
+    for a, b in zip((O, *big.backward(Q, K, V, O, G)), (o, *first)):
+        assert torch.equal(a[inside], b)
+    assert attn.sync_status() == M.MLORA_OK and big.sync_status() == M.MLORA_OK
+    attn.close()
+    big.close()
+
+
+def test_autograd_with_cut_pieces_and_two_forwards():
+    """Each graph has its own statistics and scratch: two forwards before the first backward, bf16."""
+    from adapter_gemm_packed_gb300.attention import WindowAttention
+    attn = WindowAttention([2600], 4, 1, 64, 10**6)
+    assert _parts(attn) > 1
+    x = [_draw((2600, h, 64), 70 + i, torch.bfloat16).requires_grad_() for i, h in enumerate((4, 1, 1))]
+    y = [_draw((2600, h, 64), 80 + i, torch.bfloat16).requires_grad_() for i, h in enumerate((4, 1, 1))]
+    do = _draw((2600, 4, 64), 90, torch.bfloat16)
+    a, b = attn(*x), attn(*y)
+    got = torch.autograd.grad(a, x, do) + torch.autograd.grad(b, y, 2 * do)
+    want = ()
+    for t, g in ((x, do), (y, 2 * do)):
+        t = [u.detach() for u in t]
+        o = attn.forward(*t)
+        want += attn.backward(*t, o, g)
+    assert all(torch.equal(u, w) for u, w in zip(got, want))
+    attn.close()
