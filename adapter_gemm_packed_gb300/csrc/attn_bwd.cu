@@ -445,13 +445,11 @@ __global__ void __launch_bounds__(THREADS<KEYS>, 1) k_attn_bwd(const __grid_cons
         }
         it = nx;
       }
-      if (!ok || *abort_flag) {
-        // bounded: no copy may still be writing shared memory when the block ends
-        volatile int no_abort = 0;
-        if (piece) mbar_wait(x_full, (piece - 1) & 1, &no_abort, A.err, DEV_ERR_TIMEOUT_TEARDOWN, A.timeout_ns);
-        for (int q = pos > STAGES ? pos - STAGES : 0; q < pos; ++q)
-          mbar_wait(&y_full[q % STAGES], (q / STAGES) & 1, &no_abort, A.err, DEV_ERR_TIMEOUT_TEARDOWN, A.timeout_ns);
-      }
+      // bounded: no copy may still be writing shared memory when the block ends, whoever gave up and whenever
+      volatile int no_abort = 0;
+      if (piece) mbar_wait(x_full, (piece - 1) & 1, &no_abort, A.err, DEV_ERR_TIMEOUT_TEARDOWN, A.timeout_ns);
+      for (int q = pos > STAGES ? pos - STAGES : 0; q < pos; ++q)
+        mbar_wait(&y_full[q % STAGES], (q / STAGES) & 1, &no_abort, A.err, DEV_ERR_TIMEOUT_TEARDOWN, A.timeout_ns);
     }
     __syncwarp();
   } else if (warp == 10) {

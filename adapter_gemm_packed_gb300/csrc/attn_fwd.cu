@@ -308,13 +308,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
         }
         it = nx;
       }
-      if (!ok || *abort_flag) {
-        // bounded: no copy may still be writing shared memory when the block ends
-        volatile int no_abort = 0;
-        if (nq) mbar_wait(B.q_full, (nq - 1) & 1, &no_abort, A.err, DEV_ERR_TIMEOUT_TEARDOWN, A.timeout_ns);
-        for (int q = pos > STAGES ? pos - STAGES : 0; q < pos; ++q)
-          mbar_wait(&B.kv_full[q % STAGES], (q / STAGES) & 1, &no_abort, A.err, DEV_ERR_TIMEOUT_TEARDOWN, A.timeout_ns);
-      }
+      // bounded: no copy may still be writing shared memory when the block ends, whoever gave up and whenever
+      volatile int no_abort = 0;
+      if (nq) mbar_wait(B.q_full, (nq - 1) & 1, &no_abort, A.err, DEV_ERR_TIMEOUT_TEARDOWN, A.timeout_ns);
+      for (int q = pos > STAGES ? pos - STAGES : 0; q < pos; ++q)
+        mbar_wait(&B.kv_full[q % STAGES], (q / STAGES) & 1, &no_abort, A.err, DEV_ERR_TIMEOUT_TEARDOWN, A.timeout_ns);
     }
     __syncwarp();
   } else if (warp == 10) {
