@@ -387,14 +387,11 @@ __global__ void __launch_bounds__(THREADS<KEYS>, 1) k_attn_bwd(const __grid_cons
 #pragma unroll
         for (int q = 0; q < NQ; ++q) scale32(o[q], f);
       }
-      uint32_t p[NQ][16];
-#pragma unroll
-      for (int q = 0; q < NQ; ++q) pack32(o[q], p[q]);
       if constexpr (NQ == 1) {
-        if (32 * q0 < A.D) out.put<1>(32 * q0, &p[0]);
+        if (32 * q0 < A.D) out.put<1>(32 * q0, &o[0]);
       } else {
 #pragma unroll
-        for (int q = 0; q < NQ; q += 2) out.put<2>(32 * (q0 + q), &p[q]);
+        for (int q = 0; q < NQ; q += 2) out.put<2>(32 * (q0 + q), &o[q]);
       }
       ++piece;
       it = nx;

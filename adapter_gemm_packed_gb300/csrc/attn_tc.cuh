@@ -232,10 +232,20 @@ __device__ __forceinline__ void scale32(uint32_t (&v)[32], float f) {
     v[u] = __float_as_uint(a), v[u + 1] = __float_as_uint(b);
   }
 }
-// 32 values as bf16
-__device__ __forceinline__ void pack32(const uint32_t (&v)[32], uint32_t (&p)[16]) {
-#pragma unroll
-  for (int u = 0; u < 16; ++u) p[u] = pack_bf16x2(__uint_as_float(v[2 * u]), __uint_as_float(v[2 * u + 1]));
+// Two values as bf16, to the nearest; AWAY: ties away from zero, otherwise to even.  (Rounding by adding given bits below
+// the last place and cutting off: with half a place for those bits it is rounding to the nearest.)
+template <bool AWAY>
+__device__ __forceinline__ uint32_t pack2(uint32_t lo, uint32_t hi) {
+  if constexpr (!AWAY) return pack_bf16x2(__uint_as_float(lo), __uint_as_float(hi));
+  uint32_t p;
+  asm("cvt.rs.bf16x2.f32 %0, %1, %2, %3;" : "=r"(p) : "f"(__uint_as_float(hi)), "f"(__uint_as_float(lo)), "r"(0x80008000u));
+  return p;
+}
+// columns [u, u + 8) of 32 as bf16
+template <bool AWAY>
+__device__ __forceinline__ uint4 pack8(const uint32_t (&v)[32], int u) {
+  return make_uint4(pack2<AWAY>(v[u], v[u + 1]), pack2<AWAY>(v[u + 2], v[u + 3]), pack2<AWAY>(v[u + 4], v[u + 5]),
+                    pack2<AWAY>(v[u + 6], v[u + 7]));
 }
 
 // A warp's 32 rows of an output tile (a row per lane), 32 columns at a time: through two buffers of 2 KB in shared
@@ -254,15 +264,14 @@ struct OutWarp {
   uint8_t* buf;
   int row0, h, rows, D, lane;      // the warp's first token, its head, rows that exist (32 or fewer)
   // N (one or two) runs of 32 columns from c0 on
-  template <int N>
-  __device__ __forceinline__ void put(int c0, const uint32_t (*p)[16]) {
+  template <int N, bool AWAY = false>
+  __device__ __forceinline__ void put(int c0, const uint32_t (*v)[32]) {
     if (rows < 32) {
       if (lane < rows) {
         __nv_bfloat16* y = head_row<__nv_bfloat16>(*t, row0 + lane, h) + c0;
 #pragma unroll
         for (int u = 0; u < 32 * N; u += 8)
-          if (c0 + u < D)      // D is a multiple of 8
-            *reinterpret_cast<uint4*>(y + u) = *reinterpret_cast<const uint4*>(&p[u / 32][u % 32 / 2]);
+          if (c0 + u < D) *reinterpret_cast<uint4*>(y + u) = pack8<AWAY>(v[u / 32], u % 32);      // D is a multiple of 8
       }
       return;
     }
@@ -272,8 +281,7 @@ struct OutWarp {
     for (int k = 0; k < N; ++k)
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        *reinterpret_cast<uint4*>(buf + k * OUT_BUF + lane * 64 + ((c ^ (lane >> 1 & 3)) << 4)) =
-            *reinterpret_cast<const uint4*>(&p[k][4 * c]);
+        *reinterpret_cast<uint4*>(buf + k * OUT_BUF + lane * 64 + ((c ^ (lane >> 1 & 3)) << 4)) = pack8<AWAY>(v[k], 8 * c);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if (elect_lane()) {
@@ -307,20 +315,11 @@ __device__ __forceinline__ float out_whole(uint32_t hi, uint32_t l, int k) {
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(l), "r"(0u), "r"((8 + k) * 0x1100 + k * 0x10 + 4));
   return __uint_as_float(hi + d);
 }
-// 32 outputs as bf16, to the nearest, ties away from zero: then the lower half of an output's pattern, read as signed, is the
-// difference to the rounded one, ties included.  (Rounding by adding given bits below the last place and cutting off;
-// with half a place for those bits it is rounding to the nearest.)
-__device__ __forceinline__ void pack32_away(const uint32_t (&v)[32], uint32_t (&p)[16]) {
-#pragma unroll
-  for (int u = 0; u < 16; ++u)
-    asm("cvt.rs.bf16x2.f32 %0, %1, %2, %3;"
-        : "=r"(p[u])
-        : "f"(__uint_as_float(v[2 * u + 1])), "f"(__uint_as_float(v[2 * u])), "r"(0x80008000u));
-}
 // The bytes of 32 outputs, two runs from run c on, of this lane's row, into the warp's buffer in shared memory: the
 // differences of two outputs (l), half a unit added, the upper byte kept; differences that this would carry past 127 units
-// stop there (0x7f7e: the lower one's sum may carry into the upper one).  16 sequences of 1024: bytes cut off 137.2
-// microseconds, this 139.4.
+// stop there (0x7f7e: the lower one's sum may carry into the upper one).  Outputs round ties away from zero: with ties to
+// even a lower half of 0x8000 would not say which way.  16 sequences of 1024: 142.3 microseconds with the bytes cut off
+// and ties to even, 143.8 so (the same box in turn).
 __device__ __forceinline__ void stage_out_low(uint8_t* buf, int c, const uint32_t (&v)[32], int lane) {
   const auto bytes = [&](int e) {
     const uint32_t l = __byte_perm(v[e], v[e + 1], 0x5410);
