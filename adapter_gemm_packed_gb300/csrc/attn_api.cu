@@ -87,21 +87,28 @@ void build(mlora_attention_plan_s* P, const int64_t* starts, const int32_t* lens
   // rows: of a piece; subs: pieces per tile; over: a piece's cost besides its tiles, in tiles
   auto fill = [&](WorkList& to, int rows, int subs, bool keys, int tile, int over) {
     std::vector<Cost> list;
-    for (int32_t i = 0; i < n_seqs; ++i)
+    // tiles that the piece of sequence i from row i0 on streams
+    auto cost = [&](int32_t i, int64_t i0) {
+      const int a = static_cast<int>(i0), b = static_cast<int>(std::min<int64_t>(i0 + rows, lens[i]));
+      if (!keys) return static_cast<int64_t>(key_tiles(a, b, pr.window, pr.n_sink, tile).count());
+      int lo, hi;
+      query_rows(a, b, lens[i], pr.window, pr.n_sink, lo, hi);
+      return static_cast<int64_t>((hi + tile - 1) / tile - lo / tile) * group;
+    };
+    for (int32_t i = 0; i < n_seqs; ++i) {
+      // What an ordinary piece of this sequence streams: its window, or half the sequence where that is less; at least
+      // 128 tiles.  Where so many keys are first tokens that their pieces would make more than two parts a piece, the
+      // mean, which cannot: the sums of every part lie in `saved`, a kilobyte a column.
+      int64_t usual = std::numeric_limits<int64_t>::max();
+      if (keys && !f32) {
+        usual = std::max<int64_t>(std::min<int64_t>((pr.window + 126) / 64 + 1, (lens[i] / 64 + 2) / 2) * group, 128);
+        int64_t n = 0, sum = 0, parts = 0;
+        for (int64_t i0 = 0; i0 < lens[i]; i0 += rows, ++n) sum += cost(i, i0), parts += (cost(i, i0) + usual - 1) / usual;
+        if (parts > 2 * n) usual = std::max(usual, (sum + n - 1) / n);
+      }
       for (int64_t i0 = 0; i0 < lens[i]; i0 += rows) {
-        const int a = static_cast<int>(i0), b = static_cast<int>(std::min<int64_t>(i0 + rows, lens[i]));
-        int64_t c = key_tiles(a, b, pr.window, pr.n_sink, tile).count();
-        if (keys) {
-          int lo, hi;
-          query_rows(a, b, lens[i], pr.window, pr.n_sink, lo, hi);
-          c = static_cast<int64_t>((hi + tile - 1) / tile - lo / tile) * group;
-        }
-        int64_t parts = 1;
-        if (keys && !f32) {
-          // What an ordinary piece of this sequence streams: its window, or half the sequence where that is less.
-          const int64_t usual = std::min<int64_t>((pr.window + 126) / 64 + 1, (lens[i] / 64 + 2) / 2) * group;
-          parts = std::min<int64_t>((c + std::max<int64_t>(usual, 128) - 1) / std::max<int64_t>(usual, 128), 4096);
-        }
+        const int a = static_cast<int>(i0);
+        const int64_t c = cost(i, i0), parts = keys && !f32 ? std::min<int64_t>((c + usual - 1) / usual, 4096) : 1;
         for (int h = 0; h < subs; ++h) {
           AttnItem it{static_cast<int>(starts[i]), lens[i], a, stat0[i], h, 0, static_cast<short>(parts), 0, 0};
           if (parts > 1) it.slot = P->n_slots++, it.pbase = P->n_parts, P->n_parts += static_cast<int>(parts);
@@ -111,6 +118,7 @@ void build(mlora_attention_plan_s* P, const int64_t* starts, const int32_t* lens
           }
         }
       }
+    }
     std::stable_sort(list.begin(), list.end(), [](const Cost& x, const Cost& y) { return x.c > y.c; });
     for (const AttnItem& g : gaps) list.push_back({1, g});
     const int n = static_cast<int>(list.size()), blocks = f32 ? n : std::min(n, P->sms);
