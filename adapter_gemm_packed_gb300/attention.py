@@ -9,6 +9,7 @@ in the library's kernels.  Outputs that are not given are allocated; with ``stre
 from __future__ import annotations
 
 import contextlib
+import itertools
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -204,7 +205,7 @@ class WindowAttention:
         here = "WindowAttention"
         lens = [_int32(here, "a sequence's length", n) for n in lens]
         if starts is None:
-            starts = [sum(lens[:i]) for i in range(len(lens))]
+            starts = list(itertools.accumulate(lens, initial=0))[:len(lens)]
         starts = [int(s) for s in starts]
         if len(starts) != len(lens):
             _refuse("WindowAttention", "starts and lens differ in length")

@@ -43,3 +43,15 @@ def test_ordinary_pieces_are_cut_as_before(lens, window, sinks, group):
         hi = length if i0 < sinks else min(length, min(i0 + 128, length) + window - 1)
         assert parts == -(-((-(-hi // 64) - i0 // 64) * group) // usual)
     M.mlora_attention_plan_destroy(h)
+
+
+def test_plans_of_many_samples_take_time_in_proportion():
+    """60,000 samples: a fraction of a second (adding up the lengths before each one took 20)."""
+    import time
+    from adapter_gemm_packed_gb300.attention import WindowAttention
+    t = time.perf_counter()
+    attn = WindowAttention([1, 2] * 30000, 1, 1, 64, 8, flags=M.MLORA_PLAN_HOST_ONLY)
+    assert time.perf_counter() - t < 5
+    p = M.mlora_attention_describe(attn.plan, M.MLORA_ATTN_Q_QUERIES)
+    assert attn.n == 90000 and sorted(p[0::8]) == sorted(x for i in range(30000) for x in (3 * i, 3 * i + 1))
+    attn.close()
