@@ -77,13 +77,21 @@ class DistilledAttention:
 
     def step(self, X, ids, teacher, weight=None, temperature=1.0, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
              weight_decay=0.0):
-        """One training step; returns (loss of every token, gradient at X)."""
+        """One training step; returns (loss of every token, gradient at X).  Nothing in it waits for the device: should a
+        wait inside a kernel give up (a device that does not answer; never in ordinary work), the distillation's shows as
+        NaN in the loss and so in the adapters, the others' in :meth:`sync_status`, for which a caller that keeps
+        checkpoints asks before writing one."""
         loss, dlogits = distill_loss(self.forward(X), ids, teacher, weight, temperature=temperature)
         dX = self.backward(dlogits)
         self.t += 1
         for p in self.packs:
             p.adamw(lr, betas[0], betas[1], eps, weight_decay, self.t)
         return loss, dX
+
+    def sync_status(self) -> int:
+        """Wait for the current stream; ``MLORA_ERR_TIMEOUT`` if a wait in the packs' or the attention's kernels has
+        given up since the last call, otherwise ``MLORA_OK``."""
+        return max(p.sync_status() for p in (*self.packs, self.attention))
 
     def close(self):
         for p in (*self.packs, self.attention):

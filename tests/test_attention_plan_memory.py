@@ -46,7 +46,7 @@ def test_ordinary_pieces_are_cut_as_before(lens, window, sinks, group):
 
 
 def test_plans_of_many_samples_take_time_in_proportion():
-    """60,000 samples: a fraction of a second (adding up the lengths before each one took 20)."""
+    """60,000 samples: a fraction of a second (adding up the lengths before each one took nine)."""
     import time
     from adapter_gemm_packed_gb300.attention import WindowAttention
     t = time.perf_counter()
