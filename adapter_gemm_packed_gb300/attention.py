@@ -39,11 +39,11 @@ def _heads(t, where: str, name: str, n: int, h: int, d: int, dt, dev: int) -> M.
     return M.mlora_heads(t.data_ptr(), s[0], s[1])
 
 
-def _output(t, where: str, name: str, n: int, h: int, d: int, dt, dev: int):
+def _output(t, device, where: str, name: str, n: int, h: int, d: int, dt, dev: int):
     """An output: the caller's, or a new one where that is None; and its C descriptor."""
     if t is not None:
         return t, _heads(t, where, name, n, h, d, dt, dev)
-    t = torch.empty((n, h, d), dtype=dt, device=dev)
+    t = torch.empty((n, h, d), dtype=dt, device=device)
     return t, M.mlora_heads(t.data_ptr(), h * d, d)
 
 
@@ -70,16 +70,17 @@ def _gradient(t):
 
 
 class _on:
-    """Run a call's allocations on the stream that its kernels use."""
+    """Run a call's allocations on the stream that its kernels use, of device ``dev``."""
 
-    def __init__(self, stream):
+    def __init__(self, stream, dev):
         self.ctx = None if stream is None else torch.cuda.stream(stream)
+        self.dev = dev
 
     def __enter__(self):
         if self.ctx is not None:
             self.ctx.__enter__()
         # (torch.cuda.current_stream().cuda_stream, without the two objects on the way: 0.3 microseconds for 3)
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return torch._C._cuda_getCurrentRawStream(self.dev)
 
     def __exit__(self, *exc):
         if self.ctx is not None:
@@ -102,7 +103,8 @@ def _rope_problem(where, q, k, wq, wk, cos, sin, positions, eps, interleaved, de
     if cos.dim() != 2:
         _refuse(where, "cos and sin must be [positions, rot_dim / 2]")
     rows, half = cos.shape
-    _int32(where, "the largest size", max(hq, hk, d, 2 * half, rows))
+    if hq | hk | d | half | rows >= 2**30:      # 32-bit fields, where a larger size would wrap around
+        _refuse(where, f"a size of {(hq, hk, d, rows, half)} is out of range")
     p = M.mlora_rope_problem(n, hq, hk, d, 2 * half, rows, code, M.MLORA_ROPE_INTERLEAVED if interleaved else 0, eps)
     f32 = torch.float32
     tables = (_vector(wq, where, "wq", (d,), f32, dev), _vector(wk, where, "wk", (d,), f32, dev),
@@ -118,12 +120,12 @@ def qk_norm_rope(q, k, wq, wk, cos, sin, positions, *, eps=1e-6, interleaved=Fal
     ``cos`` / ``sin`` (fp32 [positions, rot_dim / 2]) hold for the token's position (int32
     [n_tokens]).  Returns (q_out, k_out)."""
     where = "qk_norm_rope"
-    p, sq, sk, tables = _rope_problem(where, q, k, wq, wk, cos, sin, positions, eps, interleaved,
-                                      _launch_device(stream))
+    dev = _launch_device(stream)
+    p, sq, sk, tables = _rope_problem(where, q, k, wq, wk, cos, sin, positions, eps, interleaved, dev)
     hq, hk = _heads(q, where, "q", *sq), _heads(k, where, "k", *sk)
-    with _on(stream) as s:
-        q_out, oq = _output(q_out, where, "q_out", *sq)
-        k_out, ok = _output(k_out, where, "k_out", *sk)
+    with _on(stream, dev) as s:
+        q_out, oq = _output(q_out, q.device, where, "q_out", *sq)
+        k_out, ok = _output(k_out, q.device, where, "k_out", *sk)
         M.mlora_qk_norm_rope(p, hq, hk, *tables, oq, ok, s)
     return q_out, k_out
 
@@ -133,13 +135,13 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, wq, wk, cos, sin, positions, *, 
     """Gradients of :func:`qk_norm_rope` from those of its outputs and from its inputs.  Returns
     (dq, dk, dwq, dwk); the weights' gradients are None with ``weight_grads=False`` (frozen norms)."""
     where = "qk_norm_rope_backward"
-    p, sq, sk, tables = _rope_problem(where, q, k, wq, wk, cos, sin, positions, eps, interleaved,
-                                      _launch_device(stream))
+    dev = _launch_device(stream)
+    p, sq, sk, tables = _rope_problem(where, q, k, wq, wk, cos, sin, positions, eps, interleaved, dev)
     args = (_heads(dq_out, where, "dq_out", *sq), _heads(dk_out, where, "dk_out", *sk), _heads(q, where, "q", *sq),
             _heads(k, where, "k", *sk))
-    with _on(stream) as s:
-        dq, oq = _output(dq, where, "dq", *sq)
-        dk, ok = _output(dk, where, "dk", *sk)
+    with _on(stream, dev) as s:
+        dq, oq = _output(dq, q.device, where, "dq", *sq)
+        dk, ok = _output(dk, q.device, where, "dk", *sk)
         dwq = dwk = ws = None
         if weight_grads:
             dwq = torch.empty(sq[2], dtype=torch.float32, device=q.device)
@@ -232,7 +234,8 @@ class WindowAttention:
             self.plan = M.mlora_attention_plan(p, starts, lens)
         self.saved_elems = max(4, M.mlora_attention_saved_elems(self.plan))
         self.saved = None if host else self._new_saved()
-        self.qs, self.ks = ((self.n, h, self.d, self.tdtype, self.device.index) for h in (self.hq, self.hk))
+        self.dev = self.device.index or 0
+        self.qs, self.ks = ((self.n, h, self.d, self.tdtype, self.dev) for h in (self.hq, self.hk))
 
     def _new_saved(self):
         return torch.empty(self.saved_elems, dtype=torch.float32, device=self.device)
@@ -240,19 +243,19 @@ class WindowAttention:
     def _saved_ptr(self, t, where):
         """The statistics' buffer: the object's own, or the caller's, of ``saved_elems`` floats."""
         if t is None:
-            t = self.saved
-        elif not (t.dtype is torch.float32 and t.device == self.device and t.is_contiguous()
-                  and t.numel() >= self.saved_elems):
+            return None if self.saved is None else self.saved.data_ptr()
+        if not (t.dtype is torch.float32 and t.device == self.device and t.is_contiguous()
+                and t.numel() >= self.saved_elems):
             _refuse(where, f"saved must be a contiguous fp32 tensor of {self.saved_elems} elements on {self.device}")
-        return None if t is None else t.data_ptr()
+        return t.data_ptr()
 
     def forward(self, q, k, v, out=None, stream=None, saved=None):
         """Outputs [n_tokens, n_q_heads, head_dim].  ``saved`` (fp32, ``saved_elems`` elements) takes the
         statistics instead of ``self.saved``; the backward is given the same buffer."""
         w = "WindowAttention.forward"
         a = (_heads(q, w, "q", *self.qs), _heads(k, w, "k", *self.ks), _heads(v, w, "v", *self.ks))
-        with _on(stream) as s:
-            out, o = _output(out, w, "out", *self.qs)
+        with _on(stream, self.dev) as s:
+            out, o = _output(out, self.device, w, "out", *self.qs)
             M.mlora_attention_forward(self.plan, *a, o, self._saved_ptr(saved, w), s)
         return out
 
@@ -261,10 +264,10 @@ class WindowAttention:
         w = "WindowAttention.backward"
         a = (_heads(q, w, "q", *self.qs), _heads(k, w, "k", *self.ks), _heads(v, w, "v", *self.ks),
              _heads(out, w, "out", *self.qs), _heads(dout, w, "dout", *self.qs))
-        with _on(stream) as s:
-            dq, oq = _output(dq, w, "dq", *self.qs)
-            dk, ok = _output(dk, w, "dk", *self.ks)
-            dv, ov = _output(dv, w, "dv", *self.ks)
+        with _on(stream, self.dev) as s:
+            dq, oq = _output(dq, self.device, w, "dq", *self.qs)
+            dk, ok = _output(dk, self.device, w, "dk", *self.ks)
+            dv, ov = _output(dv, self.device, w, "dv", *self.ks)
             M.mlora_attention_backward(self.plan, *a, self._saved_ptr(saved, w), oq, ok, ov, s)
         return dq, dk, dv
 
@@ -272,7 +275,7 @@ class WindowAttention:
         return _AttentionFn.apply(q, k, v, self)
 
     def sync_status(self, stream=None) -> int:
-        with _on(stream) as s:
+        with _on(stream, self.dev) as s:
             return M.mlora_attention_sync_status(self.plan, s)
 
     def close(self):

@@ -34,7 +34,7 @@ def distill_loss(logits, ids, teacher, weight=None, *, temperature=1.0, grad=Tru
     a = (_vector(ids, where, "ids", (n, top), torch.int32, dev),
          _vector(teacher, where, "teacher", (n, top), torch.float32, dev),
          None if weight is None else _vector(weight, where, "weight", (n,), torch.float32, dev))
-    with _on(stream) as s:
+    with _on(stream, dev) as s:
         loss = torch.empty(n, dtype=torch.float32, device=logits.device)
         if not grad:
             dlogits = None

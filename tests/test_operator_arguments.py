@@ -32,7 +32,7 @@ def test_tensors_of_another_device_are_refused():
     assert heads(_on_gpu(1), 1).data == 4096
     for got, want in ((1, 0), (0, 1), (-1, 0)):
         _refused(lambda: heads(_on_gpu(got), want))
-        _refused(lambda: A._output(_on_gpu(got), "here", "q_out", 6, 2, 64, torch.bfloat16, want))
+        _refused(lambda: A._output(_on_gpu(got), None, "here", "q_out", 6, 2, 64, torch.bfloat16, want))
         _refused(lambda: A._vector(_on_gpu(got, (6,), torch.int32), "here", "positions", (6,), torch.int32, want))
     assert A._vector(_on_gpu(1, (6,), torch.int32), "here", "positions", (6,), torch.int32, 1) == 4096
 
