@@ -19,7 +19,7 @@
 // kernel has TMEM to spare and keeps Q and dO in it as operands (its steps took 1290 cycles from shared memory);
 // the dK / dV kernel has not.  16,384 tokens, window 4096, 64 first tokens, 16 heads of 128 on 4: 452 and 648
 // microseconds, 1.6 and 1.5 PFLOP/s of the three and four products that each does (a plain large product of the
-// library: 1.9); 9 sequences of 97 to 2501, 32 heads on 8: 131 and 177, where pieces are short.
+// library: 1.9); 9 sequences of 97 to 2501, 32 heads on 8: 133 and 178, where pieces are short.
 //
 // One block per SM walks over its share of the work list; the next piece's loads and first products run under this
 // one's last tiles and its output.

@@ -18,7 +18,7 @@
 //
 // 16,384 tokens, window 4096, 64 first tokens, 16 heads of 128 on 4: 324 microseconds, 1.5 PFLOP/s (a plain large product
 // of the library: 1.9).  Two streams' tile takes 2870 cycles, 2056 of products at the pipe's nominal rate, which the
-// library's product does not reach either.  16 sequences of 1024: 133, 0.8 PFLOP/s, bound by starts, outputs and the
+// library's product does not reach either.  16 sequences of 1024: 137, 0.8 PFLOP/s, bound by starts, outputs and the
 // hidden parts of tiles.
 //
 // Warps 0-3 and 4-7: the softmax of streams 0 and 1 and their outputs.  Warp 8: TMA loads.  Warp 9: products.

@@ -302,7 +302,7 @@ struct OutWarp {
 // same for all of a row's score gradients and does not average out.  Beside each bf16 output the forward keeps a byte:
 // the difference of its fp32 pattern to the rounded one's in units of 2^8 of the last place, to the nearest, 127 at most.
 // That leaves an error of either sign, at most 2^-16 of the output (2^-15 just below a tie), and an output that lies
-// within half a unit of a bf16 number comes back as that number.  Rows as in the statistics, 32 rows x 16 columns (bytes)
+// within half a unit of a bf16 number comes back as that number (a peaked row's dP and delta nearly cancel).  Rows as in the statistics, 32 rows x 16 columns (bytes)
 // a run, so that a warp's rows are read and written in whole lines.
 __device__ __forceinline__ uint8_t* out_low_at(const AttnArgs& A, int chunks, int h, long long s) {
   const long long r = h * A.n_stat + s;

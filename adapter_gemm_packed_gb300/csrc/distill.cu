@@ -12,7 +12,7 @@
 // which keeps its last 108 KB for the second pass; what a longer row has before that is copied again, out of L2.
 // As the second pass hands slots back, the next rows' copies fill them: reading runs under writing, and what is in
 // flight does not depend on the threads.  What a copy brings for the last time is marked to leave L2 first, so that the
-// parts of the 304 rows that come twice stay there.  8192 x 128,000 bf16 takes 723 microseconds, 5.8 TB/s of logits
+// parts of the 304 rows that come twice stay there.  8192 x 128,000 bf16 takes 720 microseconds, 5.8 TB/s of logits
 // read and gradient written (820 without the marks, when almost half as much was read from memory again; 854 with two
 // blocks an SM that load plainly and read the whole second pass out of L2); 2048 x 50,001, every fourth row without
 // weight, 89.  A block's slots are full through its first pass and refill through its second, and rows are handed out

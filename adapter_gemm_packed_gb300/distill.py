@@ -16,7 +16,11 @@ def distill_loss(logits, ids, teacher, weight=None, *, temperature=1.0, grad=Tru
 
     over each row's entries.  Returns (loss fp32 [n_tokens], dlogits): the gradient of ``loss.sum()``,
     which ``logits.backward(dlogits)`` hands on; None with ``grad=False``.  Rows of weight zero have loss
-    and gradient zero."""
+    and gradient zero.
+
+    A new ``dlogits`` is dense.  Where the logits' rows are parts of wider ones, a ``dlogits`` given with the same row stride
+    and the same offset from a 16-byte boundary is much faster (8192 x 127,993 of 128,000 columns: 0.73 milliseconds
+    against 4.6)."""
     where = "distill_loss"
     dev = _launch_device(stream)
     if logits.dim() != 2 or logits.get_device() != dev or (logits.shape[1] > 1 and logits.stride(1) != 1):

@@ -455,7 +455,9 @@ size_t mlora_qk_norm_rope_workspace(const mlora_rope_problem* problem);
  *     S = scale q k^T,  P = softmax(S over what is seen),  out = P v;
  * backward: dv = P^T dout, dP = dout v^T, dS = P (dP - rowsum(dout out)), dq = scale dS k, dk = scale dS^T q,
  * the gradients of a key / value head summed over its query heads.  Softmax statistics and sums are
- * fp32; bf16 problems round P and dS to bf16 as operands of the tensor-core products.
+ * fp32; bf16 problems round P and dS to bf16 as operands of the tensor-core products, and outputs to the
+ * nearest, ties away from zero.  The score of a row that sees one key has no gradient: dq of such a row, and dk of a
+ * key that only such rows see, are exactly zero.
  * Rows that belong to no sequence see nothing and are seen by nobody: their outputs and gradients are
  * zero, and what they hold, NaN included, reaches no other row; nor does anything cross from one
  * sequence into another.  Within a sequence a NaN or infinity may also reach rows that the window
