@@ -38,8 +38,9 @@ EXPORTS = ["mlora_plan", "mlora_plan_destroy", "mlora_forward", "mlora_backward"
            "mlora_shard_jobs", "mlora_shard_jobs_multi", "mlora_forward_w4", "mlora_backward_w4",
            "mlora_plan_grouped", "mlora_adamw_ws", "mlora_cost_estimate", "mlora_qk_norm_rope",
            "mlora_qk_norm_rope_backward", "mlora_qk_norm_rope_workspace", "mlora_attention_plan",
-           "mlora_attention_plan_destroy", "mlora_attention_saved_elems", "mlora_attention_forward",
-           "mlora_attention_backward", "mlora_attention_sync_status", "mlora_attention_describe",
+           "mlora_attention_plan_destroy", "mlora_attention_saved_elems", "mlora_attention_kept_elems",
+           "mlora_attention_workspace_elems", "mlora_attention_forward", "mlora_attention_backward",
+           "mlora_attention_backward_ws", "mlora_attention_sync_status", "mlora_attention_describe",
            "mlora_distill_loss"]
 
 
@@ -172,12 +173,15 @@ def lib() -> C.CDLL:
         L.mlora_attention_plan.restype = i32
         L.mlora_attention_plan_destroy.argtypes = [vp]
         L.mlora_attention_plan_destroy.restype = None
-        L.mlora_attention_saved_elems.argtypes = [vp]
-        L.mlora_attention_saved_elems.restype = i64
+        for f in (L.mlora_attention_saved_elems, L.mlora_attention_kept_elems, L.mlora_attention_workspace_elems):
+            f.argtypes = [vp]
+            f.restype = i64
         L.mlora_attention_forward.argtypes = [vp, H, H, H, H, vp, vp]
         L.mlora_attention_forward.restype = i32
         L.mlora_attention_backward.argtypes = [vp, H, H, H, H, H, vp, H, H, H, vp]
         L.mlora_attention_backward.restype = i32
+        L.mlora_attention_backward_ws.argtypes = [vp, H, H, H, H, H, vp, vp, H, H, H, vp]
+        L.mlora_attention_backward_ws.restype = i32
         L.mlora_attention_sync_status.argtypes = [vp, vp]
         L.mlora_attention_sync_status.restype = i32
         L.mlora_attention_describe.argtypes = [vp, i32, C.POINTER(i64), i64, C.POINTER(i64)]
@@ -367,6 +371,14 @@ def mlora_attention_saved_elems(plan: int) -> int:
     return int(lib().mlora_attention_saved_elems(plan))
 
 
+def mlora_attention_kept_elems(plan: int) -> int:
+    return int(lib().mlora_attention_kept_elems(plan))
+
+
+def mlora_attention_workspace_elems(plan: int) -> int:
+    return int(lib().mlora_attention_workspace_elems(plan))
+
+
 def mlora_attention_forward(plan, q, k, v, out, saved, stream) -> None:
     _check(lib().mlora_attention_forward(plan, q, k, v, out, saved, stream), "mlora_attention_forward")
 
@@ -374,6 +386,11 @@ def mlora_attention_forward(plan, q, k, v, out, saved, stream) -> None:
 def mlora_attention_backward(plan, q, k, v, out, dout, saved, dq, dk, dv, stream) -> None:
     _check(lib().mlora_attention_backward(plan, q, k, v, out, dout, saved, dq, dk, dv, stream),
            "mlora_attention_backward")
+
+
+def mlora_attention_backward_ws(plan, q, k, v, out, dout, saved, workspace, dq, dk, dv, stream) -> None:
+    _check(lib().mlora_attention_backward_ws(plan, q, k, v, out, dout, saved, workspace, dq, dk, dv, stream),
+           "mlora_attention_backward_ws")
 
 
 def mlora_attention_sync_status(plan, stream) -> int:

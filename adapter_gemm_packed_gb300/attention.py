@@ -232,7 +232,8 @@ class WindowAttention:
         p = M.mlora_attention_problem(self.n, self.hq, self.hk, self.d, window, n_sink, code, self.scale, flags)
         with contextlib.nullcontext() if host else torch.cuda.device(self.device):
             self.plan = M.mlora_attention_plan(p, starts, lens)
-        self.saved_elems = max(4, M.mlora_attention_saved_elems(self.plan))
+        self.saved_elems = max(4, M.mlora_attention_kept_elems(self.plan))
+        self.work_elems = M.mlora_attention_workspace_elems(self.plan)
         self.saved = None if host else self._new_saved()
         self.dev = self.device.index or 0
         self.qs, self.ks = ((self.n, h, self.d, self.tdtype, self.dev) for h in (self.hq, self.hk))
@@ -268,7 +269,10 @@ class WindowAttention:
             dq, oq = _output(dq, self.device, w, "dq", *self.qs)
             dk, ok = _output(dk, self.device, w, "dk", *self.ks)
             dv, ov = _output(dv, self.device, w, "dv", *self.ks)
-            M.mlora_attention_backward(self.plan, *a, self._saved_ptr(saved, w), oq, ok, ov, s)
+            # scratch for the sums of long pieces, handed back with the call
+            work = torch.empty(self.work_elems, dtype=torch.float32, device=self.device) if self.work_elems else None
+            M.mlora_attention_backward_ws(self.plan, *a, self._saved_ptr(saved, w),
+                                          None if work is None else work.data_ptr(), oq, ok, ov, s)
         return dq, dk, dv
 
     def __call__(self, q, k, v):

@@ -37,7 +37,7 @@ struct AttnArgs {
   mlora_heads q, k, v, o, dout, dq, dk, dv;
   float* saved;
   uint8_t* out_low;          // bf16: what the outputs' rounding cut off (see attn_tc.cuh), behind the statistics
-  int* part_cnt;             // bf16 dK / dV: counters of cut pieces, and ...
+  int* part_cnt;             // bf16 dK / dV, workspace: counters of cut pieces, and ...
   float* partials;           // ... their sums, behind that
   int n_cnt;
   int* err;

@@ -98,7 +98,7 @@ void build(mlora_attention_plan_s* P, const int64_t* starts, const int32_t* lens
     for (int32_t i = 0; i < n_seqs; ++i) {
       // What an ordinary piece of this sequence streams: its window, or half the sequence where that is less; at least
       // 128 tiles.  Where so many keys are first tokens that their pieces would make more than two parts a piece, the
-      // mean, which cannot: the sums of every part lie in `saved`, a kilobyte a column.
+      // mean, which cannot: the sums of every part take a kilobyte a column of the workspace.
       int64_t usual = std::numeric_limits<int64_t>::max();
       if (keys && !f32) {
         usual = std::max<int64_t>(std::min<int64_t>((pr.window + 126) / 64 + 1, (lens[i] / 64 + 2) / 2) * group, 128);
@@ -189,31 +189,31 @@ mlora_status check_run(const mlora_attention_plan_t* P) {
   return e == cudaSuccess ? MLORA_OK : op_cuda_fail(e, "cudaSetDevice");
 }
 
-// `saved`: the statistics; then for bf16 the outputs' low bits, the counters of cut dK / dV pieces and their sums.
+// `saved`: the statistics; then for bf16 the outputs' low bits.  The backward's workspace, there or elsewhere: the counters
+// of cut dK / dV pieces and their sums.
 struct SavedLayout {
-  int64_t low, cnt, sums, total;      // in floats
+  int64_t low, kept, sums, scratch;      // in floats
 };
 SavedLayout saved_layout(const mlora_attention_plan_t* P) {
   SavedLayout L{};
   const int64_t rows = P->n_stat * P->prob.n_q_heads, cols = P->prob.head_dim <= 64 ? 64 : 128;
   L.low = 2 * rows;
-  if (P->prob.dtype == MLORA_F32) {
-    L.cnt = L.sums = L.total = L.low;
-  } else {
-    L.cnt = L.low + rows * cols / 4;
-    L.sums = L.cnt + P->n_slots * 8;
-    L.total = L.sums + static_cast<int64_t>(P->n_parts) * 2 * 128 * cols;
+  L.kept = L.low;
+  if (P->prob.dtype == MLORA_BF16) {
+    L.kept += rows * cols / 4;
+    L.sums = static_cast<int64_t>(P->n_slots) * 8;
+    L.scratch = L.sums + static_cast<int64_t>(P->n_parts) * 2 * 128 * cols;
   }
   return L;
 }
 
-AttnArgs args_of(const mlora_attention_plan_t* P, float* saved, const WorkList& list) {
+AttnArgs args_of(const mlora_attention_plan_t* P, float* saved, float* work, const WorkList& list) {
   AttnArgs A{};
   const SavedLayout L = saved_layout(P);
   A.saved = saved;
   A.out_low = reinterpret_cast<uint8_t*>(saved + L.low);
-  A.part_cnt = reinterpret_cast<int*>(saved + L.cnt);
-  A.partials = saved + L.sums;
+  A.part_cnt = reinterpret_cast<int*>(work);
+  A.partials = work + L.sums;
   A.n_cnt = P->n_slots * 8;
   A.first = list.d_first;
   const mlora_attention_problem& p = P->prob;
@@ -302,7 +302,15 @@ void mlora_attention_plan_destroy(mlora_attention_plan_t* plan) {
 }
 
 int64_t mlora_attention_saved_elems(const mlora_attention_plan_t* plan) {
-  return plan ? saved_layout(plan).total : -1;
+  if (!plan) return -1;
+  const SavedLayout L = saved_layout(plan);
+  return L.kept + L.scratch;
+}
+
+int64_t mlora_attention_kept_elems(const mlora_attention_plan_t* plan) { return plan ? saved_layout(plan).kept : -1; }
+
+int64_t mlora_attention_workspace_elems(const mlora_attention_plan_t* plan) {
+  return plan ? saved_layout(plan).scratch : -1;
 }
 
 mlora_status mlora_attention_forward(const mlora_attention_plan_t* P, const mlora_heads* q, const mlora_heads* k,
@@ -314,7 +322,7 @@ mlora_status mlora_attention_forward(const mlora_attention_plan_t* P, const mlor
   if (st == MLORA_OK) st = check_tensor(P, out, "out", true);
   if (st != MLORA_OK) return st;
   if (!saved || !ptr_aligned(saved, 16)) return op_fail(MLORA_ERR_INVALID, "saved must be a 16-byte aligned buffer");
-  AttnArgs A = args_of(P, saved, P->f);
+  AttnArgs A = args_of(P, saved, nullptr, P->f);
   A.q = *q, A.k = *k, A.v = *v, A.o = *out;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (P->prob.dtype == MLORA_BF16) return launch_attn_fwd(A, P->f.blocks(), P->prob.n_tokens, s);
@@ -326,6 +334,14 @@ mlora_status mlora_attention_backward(const mlora_attention_plan_t* P, const mlo
                                       const mlora_heads* v, const mlora_heads* out, const mlora_heads* dout,
                                       float* saved, const mlora_heads* dq, const mlora_heads* dk,
                                       const mlora_heads* dv, void* stream) {
+  return mlora_attention_backward_ws(P, q, k, v, out, dout, saved, P && saved ? saved + saved_layout(P).kept : nullptr, dq,
+                                     dk, dv, stream);
+}
+
+mlora_status mlora_attention_backward_ws(const mlora_attention_plan_t* P, const mlora_heads* q, const mlora_heads* k,
+                                         const mlora_heads* v, const mlora_heads* out, const mlora_heads* dout,
+                                         float* saved, float* workspace, const mlora_heads* dq, const mlora_heads* dk,
+                                         const mlora_heads* dv, void* stream) {
   mlora_status st = check_run(P);
   const struct { const mlora_heads* t; const char* name; bool q; } all[] = {
       {q, "q", true}, {k, "k", false}, {v, "v", false}, {out, "out", true}, {dout, "dout", true},
@@ -334,7 +350,9 @@ mlora_status mlora_attention_backward(const mlora_attention_plan_t* P, const mlo
     if (st == MLORA_OK) st = check_tensor(P, a.t, a.name, a.q);
   if (st != MLORA_OK) return st;
   if (!saved || !ptr_aligned(saved, 16)) return op_fail(MLORA_ERR_INVALID, "saved must be a 16-byte aligned buffer");
-  AttnArgs A = args_of(P, saved, P->q), K = args_of(P, saved, P->k);
+  if (saved_layout(P).scratch && (!workspace || !ptr_aligned(workspace, 16)))
+    return op_fail(MLORA_ERR_INVALID, "the plan's cut pieces need a 16-byte aligned workspace");
+  AttnArgs A = args_of(P, saved, workspace, P->q), K = args_of(P, saved, workspace, P->k);
   for (AttnArgs* a : {&A, &K})
     a->q = *q, a->k = *k, a->v = *v, a->o = *out, a->dout = *dout, a->dq = *dq, a->dk = *dk, a->dv = *dv;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -160,7 +160,7 @@ __device__ __forceinline__ void warp_delta(const AttnArgs& A, const AttnItem& it
 }
 
 // A warp's sums of a cut piece: into the scratch, and if all parts' are there, their sum in order into o.  No warp
-// waits for another; the last one resets the counter.
+// waits for another.  (The dQ kernel, which has ended, has set the counters to zero.)
 template <int DS, int NQ>
 __device__ __forceinline__ bool join_parts(const AttnArgs& A, const AttnItem& it, int warp, int lane, uint32_t (&o)[NQ][32]) {
   constexpr int SET = 8 * 32 * 64 * DS;      // floats of one part: eight warps, 32 rows, 64 DS columns
@@ -178,7 +178,6 @@ __device__ __forceinline__ bool join_parts(const AttnArgs& A, const AttnItem& it
   if (lane == 0) last = atomicAdd(cnt, 1) == it.parts - 1;
   if (!__shfl_sync(0xffffffffu, last, 0)) return false;
   __threadfence();
-  if (lane == 0) *cnt = 0;
 #pragma unroll 1
   for (int p = 0; p < it.parts; ++p)
 #pragma unroll
@@ -250,6 +249,9 @@ __global__ void __launch_bounds__(THREADS<KEYS>, 1) k_attn_bwd(const __grid_cons
     };
     int pos = 0, tiles = 0, piece = 0;
     bool ok = true;
+    // the counters that the cut pieces of the kernel after this one start from
+    if (!KEYS && blockIdx.x == 0)
+      for (int e = tid; e < A.n_cnt; e += 256) A.part_cnt[e] = 0;
     for (int k = k_first; ok && k < k_end; ++k) {
       const AttnItem nx = next_item(k);
       const Work w = decode<KEYS>(A, it);

@@ -246,9 +246,6 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
     const int s = warp >> 2, quarter = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     int tiles = 0;
-    // the counters that the backward's cut pieces start from
-    if (blockIdx.x == 0)
-      for (int e = tid; e < A.n_cnt; e += 256) A.part_cnt[e] = 0;
     for (int k = k_first; k < k_end; ++k) {
       const AttnItem nx = next_item(k);
       const Work w = decode(F, it);

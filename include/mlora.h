@@ -484,9 +484,13 @@ mlora_status mlora_attention_plan(const mlora_attention_problem* problem, const 
                                   const int32_t* seq_len, int32_t n_seqs, mlora_attention_plan_t** out);
 void mlora_attention_plan_destroy(mlora_attention_plan_t* plan);
 
-/* Number of floats of `saved`, what the forward leaves for the backward: the softmax statistics (and
- * room for the backward's row sums), for bf16 also the bits that the outputs' rounding cut off, a
- * byte an element, and scratch of the backward.  16-byte aligned device memory. */
+/* Numbers of floats, of 16-byte aligned device memory.  kept: of `saved`, what the forward leaves for
+ * the backward: the softmax statistics (and room for the backward's row sums), for bf16 also the bits
+ * that the outputs' rounding cut off, a byte an element.  workspace: scratch of the backward alone, which any
+ * number of layers can share in turn (0 where no dk / dv piece is cut; then it may be NULL).  saved: of both in
+ * one buffer, as mlora_attention_backward takes them. */
+int64_t mlora_attention_kept_elems(const mlora_attention_plan_t* plan);
+int64_t mlora_attention_workspace_elems(const mlora_attention_plan_t* plan);
 int64_t mlora_attention_saved_elems(const mlora_attention_plan_t* plan);
 
 mlora_status mlora_attention_forward(const mlora_attention_plan_t* plan, const mlora_heads* q, const mlora_heads* k,
@@ -495,6 +499,10 @@ mlora_status mlora_attention_backward(const mlora_attention_plan_t* plan, const 
                                       const mlora_heads* v, const mlora_heads* out, const mlora_heads* dout,
                                       float* saved, const mlora_heads* dq, const mlora_heads* dk,
                                       const mlora_heads* dv, void* stream);
+mlora_status mlora_attention_backward_ws(const mlora_attention_plan_t* plan, const mlora_heads* q, const mlora_heads* k,
+                                         const mlora_heads* v, const mlora_heads* out, const mlora_heads* dout,
+                                         float* saved, float* workspace, const mlora_heads* dq, const mlora_heads* dk,
+                                         const mlora_heads* dv, void* stream);
 
 /* mlora_sync_status for an attention plan. */
 mlora_status mlora_attention_sync_status(const mlora_attention_plan_t* plan, void* stream);

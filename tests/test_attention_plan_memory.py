@@ -55,3 +55,23 @@ def test_plans_of_many_samples_take_time_in_proportion():
     p = M.mlora_attention_describe(attn.plan, M.MLORA_ATTN_Q_QUERIES)
     assert attn.n == 90000 and sorted(p[0::8]) == sorted(x for i in range(30000) for x in (3 * i, 3 * i + 1))
     attn.close()
+
+
+@pytest.mark.parametrize("dtype", [M.MLORA_BF16, M.MLORA_F32])
+def test_what_a_graph_keeps_has_no_scratch_in_it(dtype):
+    """Statistics, 8 bytes a row and head, and for bf16 a byte an output element; the sums of cut pieces are the backward's
+    workspace."""
+    from adapter_gemm_packed_gb300.attention import WindowAttention
+    for lens, cut in (([131072], True), ([300, 50], False)):
+        p = M.mlora_attention_problem(sum(lens), 32, 8, 128, 10**6, 0, dtype, 0.1, M.MLORA_PLAN_HOST_ONLY)
+        h = M.mlora_attention_plan(p, [sum(lens[:i]) for i in range(len(lens))], lens)
+        rows = sum(-(-n // 128) * 128 for n in lens)
+        kept, work = M.mlora_attention_kept_elems(h), M.mlora_attention_workspace_elems(h)
+        assert kept == rows * 32 * (2 + (128 // 4 if dtype == M.MLORA_BF16 else 0))
+        assert (work > 0) == (cut and dtype == M.MLORA_BF16)
+        assert M.mlora_attention_saved_elems(h) == kept + work
+        M.mlora_attention_plan_destroy(h)
+        attn = WindowAttention(lens, 32, 8, 128, 10**6, dtype="bf16" if dtype == M.MLORA_BF16 else "f32",
+                               flags=M.MLORA_PLAN_HOST_ONLY)
+        assert attn.saved_elems == kept
+        attn.close()

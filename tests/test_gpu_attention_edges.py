@@ -293,3 +293,33 @@ def test_autograd_with_cut_pieces_and_two_forwards():
         want += attn.backward(*t, o, g)
     assert all(torch.equal(u, w) for u, w in zip(got, want))
     attn.close()
+
+
+def test_scratch_of_the_backward():
+    """In a workspace of its own, whatever it holds, or behind what the forward left, in one buffer: the same bits.  Cut
+    pieces without a workspace are refused."""
+    from adapter_gemm_packed_gb300.attention import WindowAttention, _heads
+    attn = WindowAttention([2600], 4, 1, 64, 10**6)
+    assert attn.work_elems > 0
+    q, k, v, do = (_draw((2600, h, 64), 50 + i, torch.bfloat16) for i, h in enumerate((4, 1, 1, 4)))
+    o = attn.forward(q, k, v)
+    want = attn.backward(q, k, v, o, do)
+    both = torch.full((M.mlora_attention_saved_elems(attn.plan),), float("nan"), device="cuda")
+    got = [torch.empty_like(t) for t in (q, k, v)]
+    ins = [_heads(t, "", "", *s) for t, s in ((q, attn.qs), (k, attn.ks), (v, attn.ks), (o, attn.qs), (do, attn.qs))]
+    outs = [_heads(t, "", "", *s) for t, s in zip(got, (attn.qs, attn.ks, attn.ks))]
+    s = torch.cuda.current_stream().cuda_stream
+    M.mlora_attention_forward(attn.plan, *ins[:4], both.data_ptr(), s)
+    M.mlora_attention_backward(attn.plan, *ins, both.data_ptr(), *outs, s)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    work = torch.full((attn.work_elems,), -1, dtype=torch.int32, device="cuda")
+    for t in got:
+        t.zero_()
+    M.mlora_attention_backward_ws(attn.plan, *ins, both.data_ptr(), work.data_ptr(), *outs, s)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for bad in (None, work.data_ptr() + 4):
+        with pytest.raises(M.MloraError) as e:
+            M.mlora_attention_backward_ws(attn.plan, *ins, both.data_ptr(), bad, *outs, s)
+        assert e.value.status == M.MLORA_ERR_INVALID
+    assert attn.sync_status() == M.MLORA_OK
+    attn.close()
